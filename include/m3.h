@@ -22,8 +22,9 @@
  * m3_scan_state for the final state only), the single-token decode step
  * (m3_decode_step), the backward pass (m3_scan_bwd, m3_scan_bwd_varlen), the
  * B / C projection prep (m3_bc_prep), the block projections around the
- * layer (m3_linear, m3_mimo_up, m3_mimo_down_gate), the pieces of a sequence split across
- * ranks (m3_segment_totals, m3_state_fold), and sizing, planning and status
+ * layer (m3_linear, m3_mimo_up, m3_mimo_down_gate), the output norm
+ * (m3_group_norm_fwd, m3_group_norm_bwd and their _varlen forms), the pieces of a sequence
+ * split across ranks (m3_segment_totals, m3_state_fold), and sizing, planning and status
  * (m3_*_workspace_size, m3_scan_plan, m3_check_shape, m3_stream_status,
  * m3_status_string, m3_version).
  *
@@ -364,6 +365,76 @@ M3_API int m3_mimo_up(const m3_shape* shape, const void* x, const float* w_up, v
  *   Shape, alignment and size rules as m3_mimo_up. */
 M3_API int m3_mimo_down_gate(const m3_shape* shape, const void* Y, const float* w_down,
                              const void* z, void* out, m3_stream_t stream);
+
+/* ---- grouped norm with an activation, channels last ---------------------------
+ * The norm between the layer's output and the next projection, alone, with a
+ * SiLU after it or together with the block's gate.  Over one sample's
+ * positions and one group's channels (n = positions * channels / groups):
+ *   mean = sum x / n,  rstd = 1 / sqrt(sum (x - mean)^2 / n + eps),
+ *   u = (x - mean) rstd weight + bias,
+ *   y = u (M3_ACT_NONE), u sigma(u) (M3_ACT_SILU), u z sigma(z) (M3_ACT_GATE).
+ * seqlen = 1 makes every token its own sample (the causal form: batch =
+ * tokens); seqlen > 1 normalises over whole sequences.
+ *
+ *   shape     batch >= 1 samples, seqlen >= 0 positions of each, channels,
+ *             groups (channels % groups == 0), io_dtype, act, eps >= 0;
+ *             batch * groups < 2^31.
+ *   x, z, y   [batch][seqlen][channels] io dtype, 16-byte aligned; z with
+ *             M3_ACT_GATE only (NULL otherwise).  y may be x or z itself;
+ *             other overlaps are not allowed.
+ *   weight, bias  [channels] fp32, or NULL (1 and 0).
+ *   mean, rstd    [batch][groups] fp32, written by the forward (each may be
+ *             NULL) and read by the backward.  A sample without positions
+ *             gets 0 and 0.
+ * m3_group_norm_bwd: gradients of sum(y * dy).  dy, dx, dz in the io dtype;
+ * dweight, dbias [channels] fp32, summed over all samples and positions in a
+ * fixed order.  Each output may be NULL (not computed); dz with M3_ACT_GATE
+ * only.  No output may overlap an input or another output.
+ *   workspace  m3_group_norm_workspace_size bytes, 256-byte aligned.
+ * Any channel count and group size is taken; groups whose channels fill a
+ * multiple of 16 bytes are read and written in 16-byte pieces. */
+typedef enum { M3_ACT_NONE = 0, M3_ACT_SILU = 1, M3_ACT_GATE = 2 } m3_act;
+
+typedef struct {
+  int64_t batch;
+  int64_t seqlen;
+  int64_t channels;
+  int64_t groups;
+  int32_t io_dtype; /* m3_dtype */
+  int32_t act;      /* m3_act   */
+  float eps;
+} m3_norm_shape;
+
+/* backward, packed: whether the call is a backward one, and a _varlen one. */
+M3_API int m3_group_norm_workspace_size(const m3_norm_shape* shape, int backward, int packed,
+                                        size_t* bytes);
+
+M3_API int m3_group_norm_fwd(const m3_norm_shape* shape, const void* x, const float* weight,
+                             const float* bias, const void* z, void* y, float* mean, float* rstd,
+                             void* workspace, size_t workspace_bytes, m3_stream_t stream);
+
+M3_API int m3_group_norm_bwd(const m3_norm_shape* shape, const void* x, const float* weight,
+                             const float* bias, const void* z, const float* mean,
+                             const float* rstd, const void* dy, void* dx, float* dweight,
+                             float* dbias, void* dz, void* workspace, size_t workspace_bytes,
+                             m3_stream_t stream);
+
+/* The same over a packed batch: sample i is the rows [cu_seqlens[i],
+ * cu_seqlens[i+1]) of tensors with total_tokens rows (the rules of
+ * m3_scan_fwd_varlen, shape->seqlen being the longest sample).  Rows outside
+ * every sample are neither read nor written. */
+M3_API int m3_group_norm_fwd_varlen(const m3_norm_shape* shape, const int32_t* cu_seqlens,
+                                    int64_t total_tokens, const void* x, const float* weight,
+                                    const float* bias, const void* z, void* y, float* mean,
+                                    float* rstd, void* workspace, size_t workspace_bytes,
+                                    m3_stream_t stream);
+
+M3_API int m3_group_norm_bwd_varlen(const m3_norm_shape* shape, const int32_t* cu_seqlens,
+                                    int64_t total_tokens, const void* x, const float* weight,
+                                    const float* bias, const void* z, const float* mean,
+                                    const float* rstd, const void* dy, void* dx, float* dweight,
+                                    float* dbias, void* dz, void* workspace,
+                                    size_t workspace_bytes, m3_stream_t stream);
 
 /* ---- packed variable-length batch -------------------------------------------
  * Several sequences of different lengths in one call, stored back to back

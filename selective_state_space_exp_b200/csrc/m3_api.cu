@@ -8,7 +8,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "m3_internal.cuh"
+#include "lm_ops.cuh"
 
 namespace m3 {
 
@@ -123,6 +123,9 @@ size_t scan_workspace(const m3_shape* s, const ScanArgs& a) {
 }
 
 }  // namespace
+
+int device_status_word(int** out) { return status_word(out); }
+
 }  // namespace m3
 
 using namespace m3;

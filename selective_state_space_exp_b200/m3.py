@@ -25,6 +25,8 @@ M3_FLAG_SIMT = 1
 M3_FLAG_TEST_TIMEOUT = 2
 M3_FLAG_THETA_PER_HEAD = 4
 M3_FLAG_DY_F32 = 8
+M3_ACT_NONE, M3_ACT_SILU, M3_ACT_GATE = 0, 1, 2
+_ACTS = {"none": M3_ACT_NONE, "silu": M3_ACT_SILU, "gate": M3_ACT_GATE}
 M3_OK, M3_ERR_INVALID_ARGUMENT, M3_ERR_TIMEOUT = 0, -1, -6
 
 
@@ -56,6 +58,13 @@ class Shape(ctypes.Structure):
                 ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64),
                 ("rank", ctypes.c_int64), ("chunk", ctypes.c_int64),
                 ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class NormShape(ctypes.Structure):
+    """m3_norm_shape."""
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("channels", ctypes.c_int64), ("groups", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -120,6 +129,19 @@ def load() -> ctypes.CDLL:
             L.m3_mimo_up.restype = ctypes.c_int
             L.m3_mimo_down_gate.argtypes = [sp] + [vp] * 5
             L.m3_mimo_down_gate.restype = ctypes.c_int
+            np_ = ctypes.POINTER(NormShape)
+            L.m3_group_norm_workspace_size.argtypes = [np_, ctypes.c_int, ctypes.c_int,
+                                                       ctypes.POINTER(ctypes.c_size_t)]
+            L.m3_group_norm_fwd.argtypes = [np_] + [vp] * 8 + [ctypes.c_size_t, vp]
+            L.m3_group_norm_fwd_varlen.argtypes = [np_, vp, ctypes.c_int64] + [vp] * 8 + \
+                [ctypes.c_size_t, vp]
+            L.m3_group_norm_bwd.argtypes = [np_] + [vp] * 12 + [ctypes.c_size_t, vp]
+            L.m3_group_norm_bwd_varlen.argtypes = [np_, vp, ctypes.c_int64] + [vp] * 12 + \
+                [ctypes.c_size_t, vp]
+            for name in ("m3_group_norm_workspace_size", "m3_group_norm_fwd",
+                         "m3_group_norm_fwd_varlen", "m3_group_norm_bwd",
+                         "m3_group_norm_bwd_varlen"):
+                getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -508,3 +530,175 @@ def m3_mimo_down_gate(Y, w_down, z=None, *, out=None, stream=None):
                                   _stream(stream))
     _check("m3_mimo_down_gate", st)
     return out
+
+
+# ---- the grouped norm on the layer's output ------------------------------------
+
+def _on(stream, *tensors):
+    """Checks that the given tensors share one CUDA device and returns the
+    context in which outputs and workspaces are made and the call is issued:
+    that device's current stream, or `stream` (their memory then belongs to it)."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors are on {dev} and {t.device}")
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _expect(name, t, dtype, shape):
+    """t (None passes) has this dtype and shape."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}: expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} is {tuple(t.shape)}: expected {tuple(shape)}")
+
+
+def _norm_shape(x, groups, act, eps, scope):
+    if act not in _ACTS:
+        raise ValueError(f"act is {act!r}: expected one of {sorted(_ACTS)}")
+    C = x.shape[-1]
+    if scope == "token":
+        batch, seqlen = (x.numel() // C if C else 0), 1
+        if batch == 0:  # no token: one sample without positions
+            batch, seqlen = 1, 0
+    elif scope == "sequence":
+        if x.dim() != 3:
+            raise ValueError("scope 'sequence' takes x [batch][seqlen][channels]")
+        batch, seqlen = x.shape[0], x.shape[1]
+    else:
+        raise ValueError(f"scope is {scope!r}: expected 'token' or 'sequence'")
+    return NormShape(batch, seqlen, C, groups, _io_code(x.dtype), _ACTS[act], eps)
+
+
+def _norm_args(x, groups, weight, bias, z, act):
+    if groups < 1 or x.dim() < 1 or x.shape[-1] % groups != 0:
+        raise ValueError(f"{tuple(x.shape)} channels last do not split into {groups} groups")
+    C = x.shape[-1]
+    _expect("weight", weight, torch.float32, (C,))
+    _expect("bias", bias, torch.float32, (C,))
+    _expect("z", z, x.dtype, x.shape)
+    if (z is not None) != (act == "gate"):
+        raise ValueError("z belongs to act 'gate', and only to it")
+
+
+def _norm_workspace(shape, backward, packed, workspace, device):
+    n = ctypes.c_size_t(0)
+    _check("m3_group_norm_workspace_size", load().m3_group_norm_workspace_size(
+        ctypes.byref(shape), int(backward), int(packed), ctypes.byref(n)))
+    if workspace is None and n.value:
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=device)
+    return workspace, ctypes.c_size_t(0 if workspace is None else
+                                      workspace.numel() * workspace.element_size())
+
+
+def _norm_forward(name, shape, packed, x, weight, bias, z, y, workspace, stream, cu=None):
+    with _on(stream, x, weight, bias, z, y, workspace, cu):
+        if y is None:
+            y = torch.empty_like(x)
+        _expect("y", y, x.dtype, x.shape)
+        stat = (shape.batch if shape.seqlen or packed else 0, shape.groups)
+        mean = torch.empty(stat, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(stat, dtype=torch.float32, device=x.device)
+        workspace, nbytes = _norm_workspace(shape, False, packed, workspace, x.device)
+        pre = [_ptr(cu), ctypes.c_int64(x.shape[0])] if packed else []
+        st = getattr(load(), name)(ctypes.byref(shape), *pre, _ptr(x), _ptr(weight), _ptr(bias),
+                                   _ptr(z), _ptr(y), _ptr(mean) if mean.numel() else None,
+                                   _ptr(rstd) if rstd.numel() else None, _ptr(workspace), nbytes,
+                                   _stream(stream))
+        _check(name, st)
+    return y, mean, rstd
+
+
+def _norm_backward(name, shape, packed, x, mean, rstd, dy, weight, bias, z, workspace, stream,
+                   cu=None):
+    stat = (shape.batch if shape.seqlen or packed else 0, shape.groups)
+    _expect("mean", mean, torch.float32, stat)
+    _expect("rstd", rstd, torch.float32, stat)
+    _expect("dy", dy, x.dtype, x.shape)
+    C, f32 = x.shape[-1], torch.float32
+    with _on(stream, x, mean, rstd, dy, weight, bias, z, workspace, cu):
+        g = {"x": torch.empty_like(x), "weight": torch.empty((C,), dtype=f32, device=x.device),
+             "bias": torch.empty((C,), dtype=f32, device=x.device)}
+        if z is not None:
+            g["z"] = torch.empty_like(z)
+        workspace, nbytes = _norm_workspace(shape, True, packed, workspace, x.device)
+        pre = [_ptr(cu), ctypes.c_int64(x.shape[0])] if packed else []
+        st = getattr(load(), name)(ctypes.byref(shape), *pre, _ptr(x), _ptr(weight), _ptr(bias),
+                                   _ptr(z), _ptr(mean) if mean.numel() else None,
+                                   _ptr(rstd) if rstd.numel() else None, _ptr(dy), _ptr(g["x"]),
+                                   _ptr(g["weight"]), _ptr(g["bias"]), _ptr(g.get("z")),
+                                   _ptr(workspace), nbytes, _stream(stream))
+        _check(name, st)
+    return g
+
+
+def m3_group_norm_fwd(x, groups: int, weight=None, bias=None, z=None, *, act="none",
+                      eps: float = 1e-5, scope="token", y=None, workspace=None, stream=None):
+    """Grouped norm with an activation, channels last: x [..][C] io dtype,
+    statistics over the C / groups channels of every token (scope "token"), or
+    over all positions of a sequence too (scope "sequence", x [b][L][C]).
+    act "none", "silu", or "gate" (times silu(z), z like x); weight, bias [C]
+    fp32 or None.  Returns (y, mean, rstd), the statistics [samples][groups]."""
+    _norm_args(x, groups, weight, bias, z, act)
+    shape = _norm_shape(x, groups, act, eps, scope)
+    return _norm_forward("m3_group_norm_fwd", shape, False, x, weight, bias, z, y, workspace,
+                         stream)
+
+
+def m3_group_norm_bwd(x, groups: int, mean, rstd, dy, weight=None, bias=None, z=None, *,
+                      act="none", scope="token", workspace=None, stream=None):
+    """Backward of m3_group_norm_fwd from its inputs and statistics: a dict of
+    x and (act "gate") z in the io dtype, weight and bias fp32 [C]."""
+    _norm_args(x, groups, weight, bias, z, act)
+    shape = _norm_shape(x, groups, act, 0.0, scope)
+    return _norm_backward("m3_group_norm_bwd", shape, False, x, mean, rstd, dy, weight, bias, z,
+                          workspace, stream)
+
+
+def _norm_packed_shape(cu_seqlens, x, groups, act, eps, max_seqlen):
+    if cu_seqlens.dtype != torch.int32:
+        raise TypeError("cu_seqlens must be int32")
+    if x.dim() != 2:
+        raise ValueError("a packed batch is x [tokens][channels]")
+    S = cu_seqlens.numel() - 1
+    if S < 1:
+        raise ValueError("cu_seqlens holds no sequence")
+    if max_seqlen is None:
+        max_seqlen = int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item())
+    if act not in _ACTS:
+        raise ValueError(f"act is {act!r}: expected one of {sorted(_ACTS)}")
+    return NormShape(S, max_seqlen, x.shape[1], groups, _io_code(x.dtype), _ACTS[act], eps)
+
+
+def m3_group_norm_fwd_varlen(cu_seqlens, x, groups: int, weight=None, bias=None, z=None, *,
+                             act="none", eps: float = 1e-5, max_seqlen=None, y=None,
+                             workspace=None, stream=None):
+    """m3_group_norm_fwd over the sequences of a packed batch: x [T][C],
+    cu_seqlens [S+1] int32 on the device; max_seqlen as m3_scan_fwd_varlen.
+    Rows of y outside every sequence are left as they are."""
+    _norm_args(x, groups, weight, bias, z, act)
+    shape = _norm_packed_shape(cu_seqlens, x, groups, act, eps, max_seqlen)
+    return _norm_forward("m3_group_norm_fwd_varlen", shape, True, x, weight, bias, z, y,
+                         workspace, stream, cu_seqlens)
+
+
+def m3_group_norm_bwd_varlen(cu_seqlens, x, groups: int, mean, rstd, dy, weight=None, bias=None,
+                             z=None, *, act="none", max_seqlen=None, workspace=None, stream=None):
+    """Backward of m3_group_norm_fwd_varlen (the dict of m3_group_norm_bwd);
+    rows of dx and dz outside every sequence are undefined."""
+    _norm_args(x, groups, weight, bias, z, act)
+    shape = _norm_packed_shape(cu_seqlens, x, groups, act, 0.0, max_seqlen)
+    return _norm_backward("m3_group_norm_bwd_varlen", shape, True, x, mean, rstd, dy, weight,
+                          bias, z, workspace, stream, cu_seqlens)
