@@ -23,7 +23,9 @@
  * (m3_decode_step), the backward pass (m3_scan_bwd, m3_scan_bwd_varlen), the
  * B / C projection prep (m3_bc_prep), the block projections around the
  * layer (m3_linear, m3_mimo_up, m3_mimo_down_gate), the output norm
- * (m3_group_norm_fwd, m3_group_norm_bwd and their _varlen forms), the pieces of a sequence
+ * (m3_group_norm_fwd, m3_group_norm_bwd and their _varlen forms), the head's cross entropy
+ * (m3_linear_xent_fwd, m3_linear_xent_bwd), products with 4-bit weights (m3_linear_w4,
+ * m3_w4_quantize), the pieces of a sequence
  * split across ranks (m3_segment_totals, m3_state_fold), and sizing, planning and status
  * (m3_*_workspace_size, m3_scan_plan, m3_check_shape, m3_stream_status,
  * m3_status_string, m3_version).
@@ -435,6 +437,73 @@ M3_API int m3_group_norm_bwd_varlen(const m3_norm_shape* shape, const int32_t* c
                                     const float* rstd, const void* dy, void* dx, float* dweight,
                                     float* dbias, void* dz, void* workspace,
                                     size_t workspace_bytes, m3_stream_t stream);
+
+/* ---- softmax cross entropy of a head over a large vocabulary ------------------
+ * The loss of logits = h W^T and its gradients, from the hidden states and the
+ * head's weights: the logits are computed in tiles on the tensor cores and
+ * never stored.
+ *   lse_t = log sum_v exp(h_t . W_v),  loss_t = lse_t - h_t . W_{target_t},
+ *   0 where target_t == ignore_index;
+ *   m3_linear_xent_bwd: gradients of sum_t loss_t dloss_t; an ignored token
+ *   contributes none (its dloss is not read).
+ *   tokens >= 0, vocab >= 1, width >= 8 with width % 8 == 0; tokens, vocab,
+ *   width < 2^31 - 256.
+ *   h        [tokens][width] bf16;  W [vocab][width] bf16 (the [out][in]
+ *            layout of m3_linear); both 16-byte aligned.
+ *   targets  [tokens] int64, 8-byte aligned.  A target that is neither
+ *            ignore_index nor in [0, vocab) sets M3_ERR_INVALID_ARGUMENT in
+ *            the device error word (m3_stream_status); its loss is NaN and it
+ *            contributes no gradient.
+ *   loss, lse  [tokens] fp32 (lse also for ignored tokens); either may be NULL
+ *            in the forward; the backward reads lse.
+ *   dh [tokens][width], dW [vocab][width]  bf16, 16-byte aligned, rounded once
+ *            from fp32 sums; either may be NULL.  The gradient of each logit is
+ *            rounded to bf16 before the products that give dh and dW.
+ *   workspace  as the size queries say, 256-byte aligned.
+ * No output may overlap an input or another output.  The results of a call do
+ * not depend on what else runs: every sum has a fixed order. */
+M3_API int m3_linear_xent_fwd_workspace_size(int64_t tokens, int64_t vocab, int64_t width,
+                                             size_t* bytes);
+M3_API int m3_linear_xent_bwd_workspace_size(int64_t tokens, int64_t vocab, int64_t width,
+                                             size_t* bytes);
+
+M3_API int m3_linear_xent_fwd(int64_t tokens, int64_t vocab, int64_t width, const void* h,
+                              const void* W, const int64_t* targets, int64_t ignore_index,
+                              float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                              m3_stream_t stream);
+
+M3_API int m3_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width, const void* h,
+                              const void* W, const int64_t* targets, int64_t ignore_index,
+                              const float* lse, const float* dloss, void* dh, void* dW,
+                              void* workspace, size_t workspace_bytes, m3_stream_t stream);
+
+/* ---- products with 4-bit weights and group scales ------------------------------
+ * A projection or the head while serving, from weights held in four bits:
+ *   out[m][n] = sum_g scales[n][g] sum_{k in group g} A[m][k] (q[n][k] - z[n][g])
+ *               (+ bias[n]),
+ * fp32 sums of exact products; the weights are never rounded to bf16.
+ *   M >= 0 tokens, N >= 1 outputs, K >= group inputs, K % group == 0,
+ *   group 32, 64 or 128; M, N, K < 2^31 - 256.
+ *   A        [M][K] bf16;  out [M][N], out_dtype M3_BF16 or M3_F32.
+ *   codes    [N][K/2]: two codes q in 0..15 a byte, input 2j in the low half
+ *            of byte j.
+ *   scales   [N][K/group] bf16;  zeros [N][K/group] uint8, values 0..15 (the
+ *            low four bits are read), or NULL: every z is 8.
+ *   bias     [N] fp32 or NULL.
+ *   A, codes, out 16-byte aligned, bias 4-byte, scales 8-byte, zeros 4-byte
+ *   aligned.  out must not overlap an input. */
+M3_API int m3_linear_w4(int64_t M, int64_t N, int64_t K, int32_t group, const void* A,
+                        const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                        const float* bias, void* out, int32_t out_dtype, m3_stream_t stream);
+
+/* Codes, scales and zero points of W [N][K] (w_dtype), rounded to nearest:
+ * with zeros, scale = (max(w, 0) - min(w, 0)) / 15 of a group and zero =
+ * round(-min / scale); with zeros NULL, scale = max |w| / 7 (z = 8).  Scales
+ * are rounded to bf16 before the codes are taken from them; a group of zeros
+ * has scale 0.  W must be finite.  Sizes and alignments as m3_linear_w4 (W
+ * 4-byte aligned). */
+M3_API int m3_w4_quantize(int64_t N, int64_t K, int32_t group, int32_t w_dtype, const void* W,
+                          uint8_t* codes, void* scales, uint8_t* zeros, m3_stream_t stream);
 
 /* ---- packed variable-length batch -------------------------------------------
  * Several sequences of different lengths in one call, stored back to back

@@ -22,7 +22,7 @@ OBJ_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(LIB_DIR, "libm3_debug.so")
 SOURCES = ["m3_api.cu", "decode.cu", "scan_simt.cu", "scan_tc.cu", "scan_noalloc.cu",
            "seqpar.cu", "scan_bwd.cu", "scan_bwd_tc.cu", "bc_prep.cu", "gemm_tc.cu", "block_ops.cu",
-           "lm_api.cu", "group_norm.cu"]
+           "lm_api.cu", "group_norm.cu", "linear_xent.cu", "linear_w4.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
          "-Xptxas", "-warn-spills", "--expt-relaxed-constexpr"]

@@ -1,0 +1,669 @@
+// linear_xent.cu -- softmax cross entropy of a head over a large vocabulary, from
+// the hidden states and the head's weights; the logits are never kept.
+//
+//   l_tv = sum_k h_tk W_vk,   lse_t = log sum_v exp l_tv,
+//   loss_t = lse_t - l_{t,y_t}   (0 where y_t is the ignored target)
+//   d_tv = (exp(l_tv - lse_t) - [v = y_t]) dloss_t
+//   dh_tk = sum_v d_tv W_vk,   dW_vk = sum_t d_tv h_tk
+//
+// Everything is a matrix product on the tensor cores with an epilogue:
+//   stats    l tiles of 128 tokens x 256 classes; each tile leaves a running
+//            maximum and sum of exponentials per token (one pass over the
+//            accumulator) and the target's logit; a small kernel joins them.
+//   dlogits  the same tiles again for one piece of the vocabulary, the
+//            epilogue turning them into d / c, rounded to bf16 (the operand type
+//            of the next two products; sums stay fp32).  c is the largest
+//            |dloss|: with the usual equal dloss the targets' entries, which
+//            carry most of the gradient, are then p - 1, whose roundings differ
+//            from token to token, and not all the one rounding of dloss.
+//   grads    dW of the piece (reduction over tokens: both operands are read
+//            with the reduction as their outer dimension, MN-major) and the
+//            piece's share of dh (W MN-major), accumulated over the pieces in
+//            fp32 and rounded once.
+// The piece is chosen so that its d fits a fixed workspace.  Bound by the tensor
+// cores at training sizes: 2 M V K forward, 6 M V K backward (2 of them the
+// recomputed logits).  Where there are too few output tiles to fill the SMs the
+// reduction is split, the partial sums being added in a fixed order.
+//
+// Kernel: persistent, one CTA per SM, warp-specialised: warp 0 streams operand
+// tiles by TMA (128-byte swizzle) through a ring of stages, one thread of warp 1
+// issues tcgen05.mma into two TMEM accumulators in turn, warps 2-9 run the
+// epilogue of the other one.  Every wait is bounded (M3_ERR_TIMEOUT).
+#include <cuda.h>  // CUtensorMap
+
+#include <cstring>
+
+#include "lm_ops.cuh"
+#include "tc_ptx.cuh"
+
+namespace m3 {
+namespace {
+
+using namespace tc;
+
+constexpr int kBM = 128, kBN = 256, kBK = 64;
+constexpr int kStages = 4;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kBlk = 64 * kBK * 2;  // an MN-major block: 64 columns x 64 reduction rows
+constexpr int kBarOff = kStages * kStageBytes;
+constexpr int kSmem = kBarOff + (2 * kStages + 5) * 8 + 16;
+constexpr int kTmemCols = 2 * kBN;
+constexpr int kGroupM = 16;  // row tiles that share a column tile while it is in L2
+constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+static_assert(kSmem + 1024 <= 232448, "shared memory");
+
+enum Mode { kStats = 0, kDlogits = 1, kGrad = 2 };
+
+struct GemmArgs {
+  int64_t M, N;           // extent of the output
+  int kb, kb_per;         // reduction blocks in all, and of one split
+  int mt, nt, splits;     // tiles
+  int* status;
+  // stats, dlogits: rows are tokens, columns classes v0 + n
+  const int64_t* targets;
+  int64_t ignore, V, v0;
+  float2* stat;           // [2 nt][M]: maximum (base 2) and sum, per half tile
+  float* tlogit;          // [M]
+  const float* lse;
+  const float* dloss;
+  __nv_bfloat16* d;       // [M][ldd]
+  int64_t ldd;
+  float* unit;            // c: written by dlogits, a factor of out in grads
+  // grads
+  float* acc;             // [splits][M][N] partial sums or running sum
+  __nv_bfloat16* out;     // [M][N], written when set
+  bool add;               // acc holds an earlier sum
+};
+
+struct Maps {
+  CUtensorMap a, b;
+};
+
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+
+__device__ bool wait(uint64_t* bar, uint32_t parity, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = now_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (now_ns() - t0 > kWaitNs) {
+      if (status) atomicCAS(status, 0, (int)M3_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tma_2d(void* dst, const void* map, int c0, int c1, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+      : "memory");
+}
+
+struct Tile {
+  int m, n, split;
+};
+
+// Tiles of one split first; inside it bands of kGroupM row tiles, down each
+// column of a band before the next column: the CTAs running at one time share
+// a few row and column tiles, which stay in L2.
+__device__ __forceinline__ Tile tile_of(const GemmArgs& g, int64_t t) {
+  const int64_t per = (int64_t)g.mt * g.nt;
+  Tile o;
+  o.split = (int)(t / per);
+  const int64_t r = t % per;
+  const int64_t band = r / ((int64_t)kGroupM * g.nt);
+  const int64_t q = r % ((int64_t)kGroupM * g.nt);
+  const int rows = g.mt - (int)band * kGroupM < kGroupM ? g.mt - (int)band * kGroupM : kGroupM;
+  o.n = (int)(q / rows);
+  o.m = (int)band * kGroupM + (int)(q % rows);
+  return o;
+}
+
+// Operand tiles of one stage: K-major [rows][64] as one box; MN-major as blocks
+// of 64 columns, each 64 reduction rows of 128 bytes.
+template <bool MN, int ROWS>
+__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, int row0, int k0,
+                                             uint64_t* bar) {
+  if constexpr (MN) {
+#pragma unroll
+    for (int i = 0; i < ROWS / 64; ++i) tma_2d(dst + i * kBlk, map, row0 + i * 64, k0, bar);
+  } else {
+    tma_2d(dst, map, k0, row0, bar);
+  }
+}
+
+// The largest |dloss| of a scored token, or 1 where that is no positive finite
+// number; every epilogue thread takes part and gets it.
+__device__ __forceinline__ float largest_dloss(const GemmArgs& g, float* s_max) {
+  const int i = threadIdx.x - 64;
+  float c = 0.f;
+  for (int64_t m = i; m < g.M; m += 32 * kEpiWarps) {
+    const int64_t t = g.targets[m];
+    if (t != g.ignore && t >= 0 && t < g.V) c = fmaxf(c, fabsf(g.dloss[m]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, o));
+  if ((i & 31) == 0) s_max[i >> 5] = c;
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+  c = s_max[0];
+#pragma unroll
+  for (int w = 1; w < kEpiWarps; ++w) c = fmaxf(c, s_max[w]);
+  return c > 0.f && c < INFINITY ? c : 1.f;
+}
+
+template <int MODE>
+__device__ __forceinline__ void epilogue(const GemmArgs& g, const Tile& t, uint32_t tcol, int q,
+                                         int half, int lane, float unit) {
+  const int64_t m = (int64_t)t.m * kBM + 32 * q + lane;
+  const int64_t n0 = (int64_t)t.n * kBN + half * (kBN / 2);
+  const bool on = m < g.M;
+  if constexpr (MODE == kStats) {
+    int64_t tgt = -1;
+    if (on) tgt = g.targets[m];
+    const int64_t rel = tgt - n0;  // the target's column in this half tile
+    float mx = -INFINITY, sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < kBN / 2; c += 32) {
+      uint32_t v[32];
+      tmem_ld32(tcol + (uint32_t)c, v);
+      tmem_ld_wait();
+      float f[32];
+      float top = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        f[e] = n0 + c + e < g.V ? __uint_as_float(v[e]) : -INFINITY;
+        top = fmaxf(top, f[e]);
+      }
+      if (on && rel >= c && rel < c + 32 && tgt < g.V && tgt != g.ignore) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (rel == c + e) g.tlogit[m] = f[e];
+      }
+      const float nm = fmaxf(mx, top * kLog2e);
+      if (nm > -INFINITY) {
+        sum = sum * ex2(mx - nm);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) sum += ex2(fmaf(f[e], kLog2e, -nm));
+        mx = nm;
+      } else {  // -infinity or NaN only
+#pragma unroll
+        for (int e = 0; e < 32; ++e) sum += f[e] > -INFINITY || f[e] != f[e] ? f[e] : 0.f;
+      }
+    }
+    if (on && M3_IN((int64_t)(2 * t.n + half) * g.M + m, (int64_t)2 * g.nt * g.M, g.status))
+      g.stat[(int64_t)(2 * t.n + half) * g.M + m] = make_float2(mx, sum);
+  } else if constexpr (MODE == kDlogits) {
+    int64_t tgt = -1;
+    float scale = 0.f, off = 0.f;
+    bool live = false;
+    if (on) {
+      tgt = g.targets[m];
+      live = tgt != g.ignore && tgt >= 0 && tgt < g.V;
+      if (live) {
+        scale = __fdiv_rn(g.dloss[m], unit);
+        off = g.lse[m] * kLog2e;
+      }
+    }
+    const int64_t rel = tgt - g.v0 - n0;
+#pragma unroll 1
+    for (int c = 0; c < kBN / 2; c += 32) {
+      uint32_t v[32];
+      tmem_ld32(tcol + (uint32_t)c, v);
+      tmem_ld_wait();
+      if (!on) continue;
+      float f[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        float p = ex2(fmaf(__uint_as_float(v[e]), kLog2e, -off));
+        if (rel == c + e) p -= 1.f;
+        f[e] = live ? p * scale : 0.f;
+      }
+      __nv_bfloat16* o = g.d + m * g.ldd + n0 + c;
+#pragma unroll
+      for (int e = 0; e < 32; e += 8)
+        if (n0 + c + e < g.ldd && M3_IN(m * g.ldd + n0 + c + e + 7, g.M * g.ldd, g.status))
+          *reinterpret_cast<uint4*>(o + e) =
+              make_uint4(pack_bf16(f[e], f[e + 1]), pack_bf16(f[e + 2], f[e + 3]),
+                         pack_bf16(f[e + 4], f[e + 5]), pack_bf16(f[e + 6], f[e + 7]));
+    }
+  } else {
+    float* acc = g.acc ? g.acc + ((int64_t)t.split * g.M + m) * g.N + n0 : nullptr;
+    __nv_bfloat16* out = g.out ? g.out + m * g.N + n0 : nullptr;
+#pragma unroll 1
+    for (int c = 0; c < kBN / 2; c += 32) {
+      uint32_t v[32];
+      tmem_ld32(tcol + (uint32_t)c, v);
+      tmem_ld_wait();
+      if (!on) continue;
+#pragma unroll
+      for (int e = 0; e < 32; e += 8) {  // N is a multiple of 8
+        if (n0 + c + e >= g.N || !M3_IN(m * g.N + n0 + c + e + 7, g.M * g.N, g.status)) continue;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[e + i]);
+        if (g.add) {
+          const float4 x = *reinterpret_cast<const float4*>(acc + c + e);
+          const float4 y = *reinterpret_cast<const float4*>(acc + c + e + 4);
+          f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+          f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+        }
+        if (out) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] *= unit;
+          *reinterpret_cast<uint4*>(out + c + e) =
+              make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                         pack_bf16(f[6], f[7]));
+        } else {
+          *reinterpret_cast<float4*>(acc + c + e) = make_float4(f[0], f[1], f[2], f[3]);
+          *reinterpret_cast<float4*>(acc + c + e + 4) = make_float4(f[4], f[5], f[6], f[7]);
+        }
+      }
+    }
+  }
+}
+
+template <int MODE, bool AMN, bool BMN>
+__global__ void __launch_bounds__(kThreads, 1)
+xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t sbase = smem_u32(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if ((sbase & 1023u) != 0) {  // the swizzled layout needs 1 KB alignment
+    if (tid == 0 && g.status) atomicCAS(g.status, 0, (int)M3_ERR_CUDA);
+    return;
+  }
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kBarOff);
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* s_fin = acc_empty + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_fin + 1);
+  const int64_t tiles = (int64_t)g.mt * g.nt * g.splits;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 32 * kEpiWarps);
+    }
+    mbar_init(s_fin, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(s_tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = *s_tmem;
+
+  if (warp == 0 && lane == 0) {
+    uint32_t it = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const Tile tl = tile_of(g, t);
+      const int k0 = tl.split * g.kb_per, k1 = k0 + g.kb_per < g.kb ? k0 + g.kb_per : g.kb;
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const int s = (int)(it % kStages);
+        if (!wait(&empty[s], ((it / kStages) & 1u) ^ 1u, g.status)) { ok = false; break; }
+        uint8_t* st = sm + s * kStageBytes;
+        mbar_expect_tx(&full[s], (uint32_t)kStageBytes);
+        load_operand<AMN, kBM>(st, &maps.a, tl.m * kBM, kb * kBK, &full[s]);
+        load_operand<BMN, kBN>(st + kABytes, &maps.b, tl.n * kBN, kb * kBK, &full[s]);
+      }
+    }
+    // let the last stages' copies land (bounded) before the CTA can exit
+    for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+      wait(&full[j % kStages], (j / kStages) & 1u, g.status);
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_bf16(kBM, kBN, AMN, BMN);
+    uint32_t it = 0;
+    int j = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++j) {
+      const Tile tl = tile_of(g, t);
+      const int k0 = tl.split * g.kb_per, k1 = k0 + g.kb_per < g.kb ? k0 + g.kb_per : g.kb;
+      const int b = j & 1;
+      if (!wait(&acc_empty[b], ((j >> 1) & 1) ^ 1u, g.status)) break;
+      tc_fence_after();
+      const uint32_t dcol = tm + (uint32_t)(b * kBN);
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const int s = (int)(it % kStages);
+        if (!wait(&full[s], (it / kStages) & 1u, g.status)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t st = sbase + (uint32_t)(s * kStageBytes);
+        // K-major: 16 reduction columns are 32 bytes on; MN-major: 16 rows of 128 bytes
+        const uint64_t ad = sw128_desc(st, AMN ? kBlk : 16, 1024);
+        const uint64_t bd = sw128_desc(st + kABytes, BMN ? kBlk : 16, 1024);
+#pragma unroll
+        for (int k4 = 0; k4 < kBK / 16; ++k4)
+          mma_bf16_ss(dcol, ad + (uint64_t)(k4 * (AMN ? 128 : 2)),
+                      bd + (uint64_t)(k4 * (BMN ? 128 : 2)), idesc, kb > k0 || k4 > 0);
+        mma_commit(&empty[s]);
+      }
+      if (ok) mma_commit(&acc_full[b]);
+    }
+  } else if (warp >= 2) {
+    const int q = warp & 3;  // TMEM lane quadrant this warp may access
+    const int half = (warp - 2) >> 2;
+    float unit = 1.f;
+    if constexpr (MODE == kDlogits) {
+      __shared__ float s_max[kEpiWarps];
+      unit = largest_dloss(g, s_max);
+      if (blockIdx.x == 0 && tid == 64) *g.unit = unit;
+    }
+    if constexpr (MODE == kGrad) unit = *g.unit;
+    int j = 0;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++j) {
+      const int b = j & 1;
+      if (!wait(&acc_full[b], (j >> 1) & 1u, g.status)) break;
+      tc_fence_after();
+      epilogue<MODE>(g, tile_of(g, t),
+                     tm + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * kBN + half * (kBN / 2)), q,
+                     half, lane, unit);
+      tc_fence_before();
+      arrive(&acc_empty[b]);
+    }
+  }
+
+  // every MMA issued has completed before TMEM is released (bounded)
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    if (lane == 0) {
+      mma_commit(s_fin);
+      wait(s_fin, 0, g.status);
+    }
+    __syncwarp();
+    tmem_dealloc(tm, kTmemCols);
+  }
+}
+
+// Joins the tiles' maxima and sums of a token: 32 tokens a block, 8 warps over
+// the tiles.
+__global__ void __launch_bounds__(256)
+xent_join_kernel(const float2* stat, int parts, int64_t M, int64_t V, const int64_t* targets,
+                 int64_t ignore, const float* tlogit, float* loss, float* lse, int* status) {
+  __shared__ float2 s[8][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t m = (int64_t)blockIdx.x * 32 + lane;
+  float mx = -INFINITY, sum = 0.f;
+  if (m < M) {
+    for (int p = w; p < parts; p += 8) {
+      const float2 v = stat[(int64_t)p * M + m];
+      const float nm = fmaxf(mx, v.x);
+      if (nm > -INFINITY) {
+        sum = sum * ex2(mx - nm) + v.y * ex2(v.x - nm);
+        mx = nm;
+      } else {
+        sum += v.y;
+      }
+    }
+  }
+  s[w][lane] = make_float2(mx, sum);
+  __syncthreads();
+  if (w != 0 || m >= M) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    const float2 v = s[i][lane];
+    const float nm = fmaxf(mx, v.x);
+    if (nm > -INFINITY) {
+      sum = sum * ex2(mx - nm) + v.y * ex2(v.x - nm);
+      mx = nm;
+    } else {
+      sum += v.y;
+    }
+  }
+  const float z = (mx + log2f(sum)) * kLn2;
+  if (lse) lse[m] = z;
+  if (!loss) return;
+  const int64_t t = targets[m];
+  if (t == ignore) {
+    loss[m] = 0.f;
+  } else if (t < 0 || t >= V) {
+    if (status) atomicCAS(status, 0, (int)M3_ERR_INVALID_ARGUMENT);
+    loss[m] = __int_as_float(0x7fffffff);  // NaN
+  } else {
+    loss[m] = z - tlogit[m];
+  }
+}
+
+// out = c times the sum over splits of part[s], rounded to bf16; n is a multiple of 8.
+__global__ void __launch_bounds__(256)
+xent_sum_kernel(const float* part, int splits, int64_t n, const float* unit, __nv_bfloat16* out) {
+  const float c = *unit;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n;
+       i += (int64_t)gridDim.x * 1024) {
+    float4 f = *reinterpret_cast<const float4*>(part + i);
+    for (int s = 1; s < splits; ++s) {
+      const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)s * n + i);
+      f.x += v.x; f.y += v.y; f.z += v.z; f.w += v.w;
+    }
+    *reinterpret_cast<uint2*>(out + i) = 
+        make_uint2(pack_bf16(f.x * c, f.y * c), pack_bf16(f.z * c, f.w * c));
+  }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+// [rows][cols] bf16 with `ld` elements a row, boxes of 64 columns x box_rows.
+bool encode(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld,
+            int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One operand: [rows][cols] of memory; mn: the columns are the output's extent
+// and the rows the reduction.
+struct Operand {
+  const void* p;
+  int64_t rows, cols, ld;
+};
+
+template <int MODE, bool AMN, bool BMN>
+cudaError_t gemm(const GemmArgs& g, const Operand& a, const Operand& b, cudaStream_t s) {
+  Maps maps;
+  memset(&maps, 0, sizeof(maps));
+  if (!encode(&maps.a, a.p, a.rows, a.cols, a.ld, AMN ? kBK : kBM) ||
+      !encode(&maps.b, b.p, b.rows, b.cols, b.ld, BMN ? kBK : kBN))
+    return cudaErrorInvalidValue;
+  auto kern = xent_gemm_kernel<MODE, AMN, BMN>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 0;
+  e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)g.mt * g.nt * g.splits;
+  kern<<<(unsigned)(tiles < sms ? tiles : sms), kThreads, kSmem, s>>>(g, maps);
+  return cudaGetLastError();
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+void set_tiles(GemmArgs* g, int64_t M, int64_t N, int64_t K, int splits) {
+  g->M = M;
+  g->N = N;
+  g->mt = (int)ceil_div(M, kBM);
+  g->nt = (int)ceil_div(N, kBN);
+  g->kb = (int)ceil_div(K, kBK);
+  g->kb_per = (int)ceil_div(g->kb, splits);
+  g->splits = (int)ceil_div(g->kb, g->kb_per);
+}
+
+// Splits of a reduction of `kb` blocks over `tiles` output tiles: as many as
+// keep every SM busy, each at least four blocks long.
+int splits_for(int64_t tiles, int64_t kb) {
+  int64_t s = kPlanSms / tiles;
+  if (s > kb / 4) s = kb / 4;
+  if (s < 1) s = 1;
+  return (int)ceil_div(kb, ceil_div(kb, s));
+}
+
+// Bytes that the workspace may hold of d at a time: large enough that the
+// products over a piece fill the SMs many times, small beside the memory.
+constexpr int64_t kPieceBytes = (int64_t)256 << 20;
+
+struct BwdPlan {
+  int64_t piece, ldd;  // classes of one piece, and its row length (a multiple of 64)
+  int pieces, dh_splits, dw_splits;
+  size_t d_bytes, dh_bytes, dw_bytes;
+};
+
+BwdPlan bwd_plan(const XentArgs& a) {
+  BwdPlan p;
+  int64_t most = kPieceBytes / 2 / a.M / kBN * kBN;
+  if (most < kBN) most = kBN;
+  p.pieces = (int)ceil_div(a.V, most);
+  p.piece = ceil_div(ceil_div(a.V, p.pieces), kBN) * kBN;
+  p.pieces = (int)ceil_div(a.V, p.piece);
+  if (p.pieces == 1) p.piece = a.V;
+  p.ldd = ceil_div(p.piece, 64) * 64;
+  const int64_t kt = ceil_div(a.K, kBN);
+  p.dh_splits = splits_for(ceil_div(a.M, kBM) * kt, ceil_div(p.piece, kBK));
+  p.dw_splits = splits_for(ceil_div(p.piece, kBM) * kt, ceil_div(a.M, kBK));
+  p.d_bytes = align_up((size_t)a.M * p.ldd * 2, 256);
+  p.dh_bytes = p.pieces > 1 || p.dh_splits > 1
+                   ? align_up((size_t)p.dh_splits * a.M * a.K * 4, 256) : 0;
+  p.dw_bytes = p.dw_splits > 1 ? align_up((size_t)p.dw_splits * p.piece * a.K * 4, 256) : 0;
+  return p;
+}
+
+size_t fwd_stat_bytes(const XentArgs& a) {
+  return align_up((size_t)2 * ceil_div(a.V, kBN) * a.M * sizeof(float2), 256);
+}
+
+cudaError_t sum_splits(const float* part, int splits, int64_t n, const float* unit, void* out,
+                       cudaStream_t s) {
+  const int64_t blocks = ceil_div(n, 1024);
+  xent_sum_kernel<<<(unsigned)(blocks < kPlanSms * 8 ? blocks : kPlanSms * 8), 256, 0, s>>>(
+      part, splits, n, unit, static_cast<__nv_bfloat16*>(out));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t xent_workspace(const XentArgs& a, bool backward) {
+  if (a.M == 0) return 0;
+  if (!backward) return fwd_stat_bytes(a) + align_up((size_t)a.M * 4, 256);
+  const BwdPlan p = bwd_plan(a);
+  return p.d_bytes + p.dh_bytes + p.dw_bytes + 256;
+}
+
+cudaError_t xent_fwd_launch(const XentArgs& a, cudaStream_t s) {
+  GemmArgs g;
+  memset(&g, 0, sizeof(g));
+  set_tiles(&g, a.M, a.V, a.K, 1);
+  g.status = a.status;
+  g.targets = a.targets;
+  g.ignore = a.ignore;
+  g.V = a.V;
+  g.stat = reinterpret_cast<float2*>(a.ws);
+  g.tlogit = reinterpret_cast<float*>(a.ws + fwd_stat_bytes(a));
+  cudaError_t e = gemm<kStats, false, false>(g, Operand{a.h, a.M, a.K, a.K},
+                                             Operand{a.W, a.V, a.K, a.K}, s);
+  if (e != cudaSuccess) return e;
+  xent_join_kernel<<<(unsigned)ceil_div(a.M, 32), 256, 0, s>>>(
+      g.stat, 2 * g.nt, a.M, a.V, a.targets, a.ignore, g.tlogit, a.loss, a.lse, a.status);
+  return cudaGetLastError();
+}
+
+cudaError_t xent_bwd_launch(const XentArgs& a, cudaStream_t s) {
+  const BwdPlan p = bwd_plan(a);
+  __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(a.ws);
+  float* dh32 = reinterpret_cast<float*>(a.ws + p.d_bytes);
+  float* dw32 = reinterpret_cast<float*>(a.ws + p.d_bytes + p.dh_bytes);
+  float* unit = reinterpret_cast<float*>(a.ws + p.d_bytes + p.dh_bytes + p.dw_bytes);
+  for (int i = 0; i < p.pieces; ++i) {
+    const int64_t v0 = (int64_t)i * p.piece, n = a.V - v0 < p.piece ? a.V - v0 : p.piece;
+    const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.W) + v0 * a.K;
+    GemmArgs g;
+    memset(&g, 0, sizeof(g));
+    set_tiles(&g, a.M, n, a.K, 1);
+    g.status = a.status;
+    g.targets = a.targets;
+    g.ignore = a.ignore;
+    g.V = a.V;
+    g.v0 = v0;
+    g.lse = a.lse;
+    g.dloss = a.dloss;
+    g.d = d;
+    g.ldd = p.ldd;
+    g.unit = unit;
+    cudaError_t e = gemm<kDlogits, false, false>(g, Operand{a.h, a.M, a.K, a.K},
+                                                 Operand{W, n, a.K, a.K}, s);
+    if (e != cudaSuccess) return e;
+    if (a.dW) {  // [n][K] = d^T h
+      GemmArgs w;
+      memset(&w, 0, sizeof(w));
+      set_tiles(&w, n, a.K, a.M, p.dw_splits);
+      w.status = a.status;
+      w.unit = unit;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dW) + v0 * a.K;
+      if (w.splits > 1) w.acc = dw32; else w.out = out;
+      e = gemm<kGrad, true, true>(w, Operand{d, a.M, n, p.ldd}, Operand{a.h, a.M, a.K, a.K}, s);
+      if (e == cudaSuccess && w.splits > 1) e = sum_splits(dw32, w.splits, n * a.K, unit, out, s);
+      if (e != cudaSuccess) return e;
+    }
+    if (a.dh) {  // [M][K] += d W
+      GemmArgs h;
+      memset(&h, 0, sizeof(h));
+      set_tiles(&h, a.M, a.K, n, p.dh_splits);
+      h.status = a.status;
+      h.unit = unit;
+      const bool last = i + 1 == p.pieces;
+      h.add = i > 0;
+      if (p.dh_bytes) h.acc = dh32;
+      if (last && p.dh_splits == 1) h.out = static_cast<__nv_bfloat16*>(a.dh);
+      e = gemm<kGrad, false, true>(h, Operand{d, a.M, n, p.ldd}, Operand{W, n, a.K, a.K}, s);
+      if (e == cudaSuccess && last && p.dh_splits > 1)
+        e = sum_splits(dh32, p.dh_splits, a.M * a.K, unit, a.dh, s);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+}  // namespace m3

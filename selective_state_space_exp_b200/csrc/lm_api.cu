@@ -133,6 +133,72 @@ int norm_call(const m3_norm_shape* s, const int32_t* cu, int64_t tokens, bool va
   return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;
 }
 
+int check_xent(int64_t M, int64_t V, int64_t K) {
+  if (M < 0 || V < 1 || K < 8) return M3_ERR_INVALID_ARGUMENT;
+  const int64_t most = kMaxExtent - 256;
+  if (K % 8 != 0 || M >= most || V >= most || K >= most) return M3_ERR_UNSUPPORTED;
+  if (M > kMaxElems / V || M > kMaxElems / K || V > kMaxElems / K) return M3_ERR_UNSUPPORTED;
+  return M3_OK;
+}
+
+int xent_size(int64_t M, int64_t V, int64_t K, bool backward, size_t* bytes) {
+  int st = check_xent(M, V, K);
+  if (st != M3_OK) return st;
+  if (!bytes) return M3_ERR_INVALID_ARGUMENT;
+  XentArgs a;
+  memset(&a, 0, sizeof(a));
+  a.M = M; a.V = V; a.K = K;
+  *bytes = xent_workspace(a, backward);
+  return M3_OK;
+}
+
+int xent_call(XentArgs a, void* ws, size_t ws_bytes, bool backward, m3_stream_t stream) {
+  int st = check_xent(a.M, a.V, a.K);
+  if (st != M3_OK) return st;
+  const int64_t M = a.M, V = a.V, K = a.K;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (!a.h && M > 0) return M3_ERR_INVALID_ARGUMENT;
+  if (M > 0 && (!a.W || !a.targets)) return M3_ERR_INVALID_ARGUMENT;
+  if (M > 0 && backward && (!a.lse || !a.dloss)) return M3_ERR_INVALID_ARGUMENT;
+  for (const void* p : {a.h, a.W, (const void*)a.dh, (const void*)a.dW})
+    if (p && !is_aligned(p, 16)) return M3_ERR_ALIGNMENT;
+  if (a.targets && !is_aligned(a.targets, 8)) return M3_ERR_ALIGNMENT;
+  for (const void* p : {(const void*)a.loss, (const void*)a.lse, (const void*)a.dloss})
+    if (p && !is_aligned(p, 4)) return M3_ERR_ALIGNMENT;
+  const size_t nh = (size_t)M * K * 2, nw = (size_t)V * K * 2, nt = (size_t)M * 4;
+  const Span in[] = {{a.h, nh}, {a.W, nw}, {a.targets, (size_t)M * 8}, {a.dloss, nt},
+                     {backward ? a.lse : nullptr, nt}};
+  const Span out[] = {{a.loss, nt}, {backward ? nullptr : a.lse, nt}, {a.dh, nh}, {a.dW, nw},
+                      {ws, ws_bytes}};
+  for (const Span& o : out) {
+    for (const Span& i : in)
+      if (overlap(o, i)) return M3_ERR_INVALID_ARGUMENT;
+    for (const Span& q : out)
+      if (&o != &q && overlap(o, q)) return M3_ERR_INVALID_ARGUMENT;
+  }
+  if (M == 0) {  // no token: the weights' gradient is zero
+    if (a.dW && cudaMemsetAsync(a.dW, 0, nw, cs) != cudaSuccess) return M3_ERR_CUDA;
+    return M3_OK;
+  }
+  if (backward ? (!a.dh && !a.dW) : (!a.loss && !a.lse)) return M3_OK;
+  const size_t need = xent_workspace(a, backward);
+  if (!ws || ws_bytes < need || !is_aligned(ws, 256)) return M3_ERR_WORKSPACE;
+  a.ws = static_cast<char*>(ws);
+  if (device_status_word(&a.status) != M3_OK) return M3_ERR_CUDA;
+  const cudaError_t e = backward ? xent_bwd_launch(a, cs) : xent_fwd_launch(a, cs);
+  return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+}
+
+int check_w4(int64_t M, int64_t N, int64_t K, int32_t group) {
+  if (M < 0 || N < 1 || K < 1 || group < 1) return M3_ERR_INVALID_ARGUMENT;
+  if (group != 32 && group != 64 && group != 128) return M3_ERR_UNSUPPORTED;
+  if (K % group != 0) return M3_ERR_INVALID_ARGUMENT;
+  const int64_t most = kMaxExtent - 256;
+  if (M >= most || N >= most || K >= most) return M3_ERR_UNSUPPORTED;
+  if (N > kMaxElems / K || M > kMaxElems / K || M > kMaxElems / N) return M3_ERR_UNSUPPORTED;
+  return M3_OK;
+}
+
 }  // namespace
 }  // namespace m3
 
@@ -193,6 +259,92 @@ M3_API int m3_group_norm_bwd_varlen(const m3_norm_shape* s, const int32_t* cu_se
                   const_cast<float*>(rstd), dweight, dbias};
   return norm_call(s, cu_seqlens, total_tokens, true, io, true, workspace, workspace_bytes,
                    stream);
+}
+
+M3_API int m3_linear_xent_fwd_workspace_size(int64_t tokens, int64_t vocab, int64_t width,
+                                             size_t* bytes) {
+  return xent_size(tokens, vocab, width, false, bytes);
+}
+
+M3_API int m3_linear_xent_bwd_workspace_size(int64_t tokens, int64_t vocab, int64_t width,
+                                             size_t* bytes) {
+  return xent_size(tokens, vocab, width, true, bytes);
+}
+
+M3_API int m3_linear_xent_fwd(int64_t tokens, int64_t vocab, int64_t width, const void* h,
+                              const void* W, const int64_t* targets, int64_t ignore_index,
+                              float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                              m3_stream_t stream) {
+  m3::Range range_("m3_linear_xent_fwd");
+  XentArgs a;
+  memset(&a, 0, sizeof(a));
+  a.M = tokens; a.V = vocab; a.K = width;
+  a.h = h; a.W = W; a.targets = targets; a.ignore = ignore_index;
+  a.loss = loss; a.lse = lse;
+  return xent_call(a, workspace, workspace_bytes, false, stream);
+}
+
+M3_API int m3_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width, const void* h,
+                              const void* W, const int64_t* targets, int64_t ignore_index,
+                              const float* lse, const float* dloss, void* dh, void* dW,
+                              void* workspace, size_t workspace_bytes, m3_stream_t stream) {
+  m3::Range range_("m3_linear_xent_bwd");
+  XentArgs a;
+  memset(&a, 0, sizeof(a));
+  a.M = tokens; a.V = vocab; a.K = width;
+  a.h = h; a.W = W; a.targets = targets; a.ignore = ignore_index;
+  a.lse = const_cast<float*>(lse);
+  a.dloss = dloss; a.dh = dh; a.dW = dW;
+  return xent_call(a, workspace, workspace_bytes, true, stream);
+}
+
+M3_API int m3_linear_w4(int64_t M, int64_t N, int64_t K, int32_t group, const void* A,
+                        const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                        const float* bias, void* out, int32_t out_dtype, m3_stream_t stream) {
+  m3::Range range_("m3_linear_w4");
+  int st = check_w4(M, N, K, group);
+  if (st != M3_OK) return st;
+  if (out_dtype != M3_BF16 && out_dtype != M3_F32) return M3_ERR_INVALID_ARGUMENT;
+  if (M == 0) return M3_OK;
+  if (!A || !codes || !scales || !out) return M3_ERR_INVALID_ARGUMENT;
+  if (!is_aligned(A, 16) || !is_aligned(codes, 16) || !is_aligned(out, 16) ||
+      !is_aligned(scales, 8) || !is_aligned(zeros, 4) || !is_aligned(bias, 4))
+    return M3_ERR_ALIGNMENT;
+  const size_t groups = (size_t)N * (K / group);
+  const Span o{out, (size_t)M * N * (out_dtype == M3_F32 ? 4 : 2)};
+  for (const Span& i : {Span{A, (size_t)M * K * 2}, Span{codes, (size_t)N * (K / 2)},
+                        Span{scales, groups * 2}, Span{zeros, groups}, Span{bias, (size_t)N * 4}})
+    if (overlap(o, i)) return M3_ERR_INVALID_ARGUMENT;
+  W4Args a;
+  a.M = M; a.N = N; a.K = K; a.group = group;
+  a.A = A; a.codes = codes; a.scales = scales; a.zeros = zeros; a.bias = bias;
+  a.out = out; a.out_f32 = out_dtype == M3_F32;
+  if (device_status_word(&a.status) != M3_OK) return M3_ERR_CUDA;
+  const cudaError_t e = w4_launch(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+}
+
+M3_API int m3_w4_quantize(int64_t N, int64_t K, int32_t group, int32_t w_dtype, const void* W,
+                          uint8_t* codes, void* scales, uint8_t* zeros, m3_stream_t stream) {
+  m3::Range range_("m3_w4_quantize");
+  int st = check_w4(1, N, K, group);
+  if (st != M3_OK) return st;
+  if (w_dtype != M3_BF16 && w_dtype != M3_F32) return M3_ERR_INVALID_ARGUMENT;
+  if (!W || !codes || !scales) return M3_ERR_INVALID_ARGUMENT;
+  if (!is_aligned(W, 4) || !is_aligned(codes, 16) || !is_aligned(scales, 8) ||
+      !is_aligned(zeros, 4))
+    return M3_ERR_ALIGNMENT;
+  const size_t groups = (size_t)N * (K / group);
+  const Span w{W, (size_t)N * K * (w_dtype == M3_F32 ? 4 : 2)};
+  const Span out[] = {{codes, (size_t)N * (K / 2)}, {scales, groups * 2}, {zeros, groups}};
+  for (const Span& o : out) {
+    if (overlap(o, w)) return M3_ERR_INVALID_ARGUMENT;
+    for (const Span& q : out)
+      if (&o != &q && overlap(o, q)) return M3_ERR_INVALID_ARGUMENT;
+  }
+  const cudaError_t e = w4_quantize_launch(N, K, group, w_dtype == M3_BF16, W, codes, scales,
+                                           zeros, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -43,4 +43,41 @@ size_t group_norm_workspace(const NormArgs& a, bool backward);
 cudaError_t group_norm_fwd_launch(const NormArgs& a, cudaStream_t s);
 cudaError_t group_norm_bwd_launch(const NormArgs& a, cudaStream_t s);
 
+// Softmax cross entropy of logits = h W^T, never stored: M tokens, V classes,
+// width K.
+struct XentArgs {
+  int64_t M, V, K;
+  const void* h;  // [M][K] bf16
+  const void* W;  // [V][K] bf16
+  const int64_t* targets;
+  int64_t ignore;
+  float* loss;       // [M] (forward)
+  float* lse;        // [M] (written by the forward, read by the backward)
+  const float* dloss;  // [M]
+  void* dh;          // [M][K] bf16 or nullptr
+  void* dW;          // [V][K] bf16 or nullptr
+  char* ws;
+  int* status;
+};
+size_t xent_workspace(const XentArgs& a, bool backward);
+cudaError_t xent_fwd_launch(const XentArgs& a, cudaStream_t s);
+cudaError_t xent_bwd_launch(const XentArgs& a, cudaStream_t s);
+
+// out = A Wq^T (+ bias) with 4-bit weights: M tokens, N outputs, K inputs.
+struct W4Args {
+  int64_t M, N, K;
+  int group;
+  const void* A;          // [M][K] bf16
+  const uint8_t* codes;   // [N][K / 2], the even input low
+  const void* scales;     // [N][K / group] bf16
+  const uint8_t* zeros;   // [N][K / group] or nullptr (8)
+  const float* bias;      // [N] or nullptr
+  void* out;              // [M][N]
+  bool out_f32;
+  int* status;
+};
+cudaError_t w4_launch(const W4Args& a, cudaStream_t s);
+cudaError_t w4_quantize_launch(int64_t N, int64_t K, int group, bool bf16, const void* W,
+                               uint8_t* codes, void* scales, uint8_t* zeros, cudaStream_t s);
+
 }  // namespace m3

@@ -138,9 +138,21 @@ def load() -> ctypes.CDLL:
             L.m3_group_norm_bwd.argtypes = [np_] + [vp] * 12 + [ctypes.c_size_t, vp]
             L.m3_group_norm_bwd_varlen.argtypes = [np_, vp, ctypes.c_int64] + [vp] * 12 + \
                 [ctypes.c_size_t, vp]
+            i64 = ctypes.c_int64
+            for name in ("m3_linear_xent_fwd_workspace_size", "m3_linear_xent_bwd_workspace_size"):
+                getattr(L, name).argtypes = [i64] * 3 + [ctypes.POINTER(ctypes.c_size_t)]
+            L.m3_linear_xent_fwd.argtypes = [i64] * 3 + [vp] * 3 + [i64] + [vp] * 3 + \
+                [ctypes.c_size_t, vp]
+            L.m3_linear_xent_bwd.argtypes = [i64] * 3 + [vp] * 3 + [i64] + [vp] * 5 + \
+                [ctypes.c_size_t, vp]
+            L.m3_linear_w4.argtypes = [i64] * 3 + [ctypes.c_int32] + [vp] * 6 + \
+                [ctypes.c_int32, vp]
+            L.m3_w4_quantize.argtypes = [i64] * 2 + [ctypes.c_int32] * 2 + [vp] * 5
             for name in ("m3_group_norm_workspace_size", "m3_group_norm_fwd",
                          "m3_group_norm_fwd_varlen", "m3_group_norm_bwd",
-                         "m3_group_norm_bwd_varlen"):
+                         "m3_group_norm_bwd_varlen", "m3_linear_xent_fwd_workspace_size",
+                         "m3_linear_xent_bwd_workspace_size", "m3_linear_xent_fwd",
+                         "m3_linear_xent_bwd", "m3_linear_w4", "m3_w4_quantize"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -702,3 +714,121 @@ def m3_group_norm_bwd_varlen(cu_seqlens, x, groups: int, mean, rstd, dy, weight=
     shape = _norm_packed_shape(cu_seqlens, x, groups, act, 0.0, max_seqlen)
     return _norm_backward("m3_group_norm_bwd_varlen", shape, True, x, mean, rstd, dy, weight,
                           bias, z, workspace, stream, cu_seqlens)
+
+
+# ---- the head's cross entropy ---------------------------------------------------
+
+def _xent_args(h, W, targets):
+    if h.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
+        raise TypeError("the head takes bf16 h and W")
+    if targets.dtype != torch.int64:
+        raise TypeError(f"targets is {targets.dtype}: expected {torch.int64}")
+    if W.dim() != 2 or h.dim() < 1 or h.shape[-1] != W.shape[1]:
+        raise ValueError(f"h is {tuple(h.shape)} and W {tuple(W.shape)}: expected [..][K], [V][K]")
+    if targets.shape != h.shape[:-1]:
+        raise ValueError(f"targets is {tuple(targets.shape)}: expected {tuple(h.shape[:-1])}")
+    return targets.numel(), W.shape[0], W.shape[1]
+
+
+def _xent_workspace(name, sizes, workspace, device):
+    n = ctypes.c_size_t(0)
+    _check(name, getattr(load(), name)(*sizes, ctypes.byref(n)))
+    if workspace is None and n.value:
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=device)
+    return workspace, ctypes.c_size_t(0 if workspace is None else
+                                      workspace.numel() * workspace.element_size())
+
+
+def m3_linear_xent_fwd(h, W, targets, *, ignore_index: int = -100, workspace=None, stream=None):
+    """Softmax cross entropy of logits = h W^T, which are never stored: h [..][K]
+    bf16, W [V][K] bf16, targets [..] int64 (ignore_index: not scored).  Returns
+    (loss, lse), fp32 and shaped like targets."""
+    sizes = [ctypes.c_int64(v) for v in _xent_args(h, W, targets)]
+    with _on(stream, h, W, targets, workspace):
+        loss = torch.empty(targets.shape, dtype=torch.float32, device=h.device)
+        lse = torch.empty(targets.shape, dtype=torch.float32, device=h.device)
+        workspace, nbytes = _xent_workspace("m3_linear_xent_fwd_workspace_size", sizes, workspace,
+                                            h.device)
+        st = load().m3_linear_xent_fwd(*sizes, _ptr(h), _ptr(W), _ptr(targets),
+                                       ctypes.c_int64(ignore_index), _ptr(loss), _ptr(lse),
+                                       _ptr(workspace), nbytes, _stream(stream))
+        _check("m3_linear_xent_fwd", st)
+    return loss, lse
+
+
+def m3_linear_xent_bwd(h, W, targets, lse, dloss, *, ignore_index: int = -100, want_dh=True,
+                       want_dW=True, workspace=None, stream=None):
+    """Backward of m3_linear_xent_fwd: (dh, dW) bf16, the gradients of
+    sum(loss * dloss) (None for one that is not wanted).  lse as the forward
+    gave it, dloss fp32 shaped like targets."""
+    sizes = [ctypes.c_int64(v) for v in _xent_args(h, W, targets)]
+    _expect("lse", lse, torch.float32, targets.shape)
+    _expect("dloss", dloss, torch.float32, targets.shape)
+    with _on(stream, h, W, targets, lse, dloss, workspace):
+        dh = torch.empty_like(h) if want_dh else None
+        dW = torch.empty_like(W) if want_dW else None
+        workspace, nbytes = _xent_workspace("m3_linear_xent_bwd_workspace_size", sizes, workspace,
+                                            h.device)
+        st = load().m3_linear_xent_bwd(*sizes, _ptr(h), _ptr(W), _ptr(targets),
+                                       ctypes.c_int64(ignore_index), _ptr(lse), _ptr(dloss),
+                                       _ptr(dh), _ptr(dW), _ptr(workspace), nbytes,
+                                       _stream(stream))
+        _check("m3_linear_xent_bwd", st)
+    return dh, dW
+
+
+# ---- 4-bit weights ---------------------------------------------------------------
+
+def m3_w4_quantize(W, group: int = 128, *, symmetric=False, stream=None):
+    """W [N][K] (bf16 or fp32) in four bits with one scale for every `group`
+    inputs: (codes [N][K/2] uint8, scales [N][K/group] bf16, zeros [N][K/group]
+    uint8, or None when symmetric)."""
+    if W.dim() != 2:
+        raise ValueError(f"W is {tuple(W.shape)}: expected [N][K]")
+    N, K = W.shape
+    if group not in (32, 64, 128) or K % group != 0 or K == 0:
+        raise ValueError(f"{K} inputs do not split into groups of {group} (32, 64 or 128)")
+    with _on(stream, W):
+        codes = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
+        scales = torch.empty((N, K // group), dtype=torch.bfloat16, device=W.device)
+        zeros = None if symmetric else torch.empty((N, K // group), dtype=torch.uint8,
+                                                   device=W.device)
+        st = load().m3_w4_quantize(ctypes.c_int64(N), ctypes.c_int64(K), ctypes.c_int32(group),
+                                   ctypes.c_int32(_io_code(W.dtype)), _ptr(W), _ptr(codes),
+                                   _ptr(scales), _ptr(zeros), _stream(stream))
+        _check("m3_w4_quantize", st)
+    return codes, scales, zeros
+
+
+def m3_linear_w4(A, codes, scales, zeros=None, bias=None, *, out=None, out_dtype=torch.bfloat16,
+                 stream=None):
+    """out = A W^T (+ bias) with W held in four bits (m3_w4_quantize's layout):
+    A [..][K] bf16, codes [N][K/2] uint8, scales [N][K/group] bf16, zeros
+    [N][K/group] uint8 or None (8); returns out [..][N] in out_dtype (bf16 or
+    fp32)."""
+    if A.dtype != torch.bfloat16:
+        raise TypeError(f"A is {A.dtype}: expected {torch.bfloat16}")
+    if codes.dim() != 2 or scales.dim() != 2:
+        raise ValueError("codes and scales are [N][..]")
+    N, K = codes.shape[0], 2 * codes.shape[1]
+    _expect("codes", codes, torch.uint8, (N, K // 2))
+    if A.dim() < 1 or A.shape[-1] != K:
+        raise ValueError(f"A is {tuple(A.shape)}: expected [..][{K}]")
+    if scales.shape[1] == 0 or K % scales.shape[1] != 0:
+        raise ValueError(f"scales is {tuple(scales.shape)} for {K} inputs")
+    _expect("scales", scales, torch.bfloat16, (N, scales.shape[1]))
+    _expect("zeros", zeros, torch.uint8, scales.shape)
+    _expect("bias", bias, torch.float32, (N,))
+    if out is not None:
+        out_dtype = out.dtype
+    code = _io_code(out_dtype)
+    with _on(stream, A, codes, scales, zeros, bias, out):
+        if out is None:
+            out = torch.empty(A.shape[:-1] + (N,), dtype=out_dtype, device=A.device)
+        _expect("out", out, out_dtype, A.shape[:-1] + (N,))
+        st = load().m3_linear_w4(ctypes.c_int64(A.numel() // K), ctypes.c_int64(N),
+                                 ctypes.c_int64(K), ctypes.c_int32(K // scales.shape[1]), _ptr(A),
+                                 _ptr(codes), _ptr(scales), _ptr(zeros), _ptr(bias), _ptr(out),
+                                 ctypes.c_int32(code), _stream(stream))
+        _check("m3_linear_w4", st)
+    return out
