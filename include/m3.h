@@ -490,8 +490,8 @@ M3_API int m3_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width, cons
  *   scales   [N][K/group] bf16;  zeros [N][K/group] uint8, values 0..15 (the
  *            low four bits are read), or NULL: every z is 8.
  *   bias     [N] fp32 or NULL.
- *   A, codes, out 16-byte aligned, bias 4-byte, scales 8-byte, zeros 4-byte
- *   aligned.  out must not overlap an input. */
+ *   A, codes, scales, zeros, out 16-byte aligned, bias 4-byte aligned.  out
+ *   must not overlap an input. */
 M3_API int m3_linear_w4(int64_t M, int64_t N, int64_t K, int32_t group, const void* A,
                         const uint8_t* codes, const void* scales, const uint8_t* zeros,
                         const float* bias, void* out, int32_t out_dtype, m3_stream_t stream);

@@ -308,7 +308,7 @@ M3_API int m3_linear_w4(int64_t M, int64_t N, int64_t K, int32_t group, const vo
   if (M == 0) return M3_OK;
   if (!A || !codes || !scales || !out) return M3_ERR_INVALID_ARGUMENT;
   if (!is_aligned(A, 16) || !is_aligned(codes, 16) || !is_aligned(out, 16) ||
-      !is_aligned(scales, 8) || !is_aligned(zeros, 4) || !is_aligned(bias, 4))
+      !is_aligned(scales, 16) || !is_aligned(zeros, 16) || !is_aligned(bias, 4))
     return M3_ERR_ALIGNMENT;
   const size_t groups = (size_t)N * (K / group);
   const Span o{out, (size_t)M * N * (out_dtype == M3_F32 ? 4 : 2)};
@@ -331,8 +331,8 @@ M3_API int m3_w4_quantize(int64_t N, int64_t K, int32_t group, int32_t w_dtype, 
   if (st != M3_OK) return st;
   if (w_dtype != M3_BF16 && w_dtype != M3_F32) return M3_ERR_INVALID_ARGUMENT;
   if (!W || !codes || !scales) return M3_ERR_INVALID_ARGUMENT;
-  if (!is_aligned(W, 4) || !is_aligned(codes, 16) || !is_aligned(scales, 8) ||
-      !is_aligned(zeros, 4))
+  if (!is_aligned(W, 4) || !is_aligned(codes, 16) || !is_aligned(scales, 16) ||
+      !is_aligned(zeros, 16))
     return M3_ERR_ALIGNMENT;
   const size_t groups = (size_t)N * (K / group);
   const Span w{W, (size_t)N * K * (w_dtype == M3_F32 ? 4 : 2)};

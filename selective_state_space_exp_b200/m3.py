@@ -8,6 +8,7 @@ the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -74,6 +75,8 @@ _lock = threading.Lock()
 def load() -> ctypes.CDLL:
     """Load libm3.so (built by __graft_entry__.build() or _build.py)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -544,116 +547,131 @@ def m3_mimo_down_gate(Y, w_down, z=None, *, out=None, stream=None):
     return out
 
 
+# ---- operators between the layer and a model's tokens ---------------------------
+# Their calls can be as short as a few microseconds on the device, so the
+# marshalling below keeps to plain integers, and shapes and workspace sizes are
+# looked up once per set of extents.
+
+def _enter(stream, device):
+    """The context a call is issued in (None: the current one will do) and its
+    stream handle.  Outputs and workspaces are made inside the context, so with
+    an explicit stream their memory belongs to that stream."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream), stream.cuda_stream
+    raw = torch._C._cuda_getCurrentRawStream(device.index)
+    if device.index == torch.cuda.current_device():
+        return None, raw
+    return torch.cuda.device(device), raw
+
+
+def _device_of(t):
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    return t.device
+
+
+def _addr(name, t, dtype, shape, device):
+    """Address of t after checks of its type, shape, device and layout; None passes."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}: expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} is {tuple(t.shape)}: expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}: expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _scratch(nbytes, workspace, device):
+    """(address, bytes, the tensor to keep alive) of a call's workspace."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0, None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _run_in(ctx, fn):
+    if ctx is None:
+        return fn()
+    with ctx:
+        return fn()
+
+
 # ---- the grouped norm on the layer's output ------------------------------------
 
-def _on(stream, *tensors):
-    """Checks that the given tensors share one CUDA device and returns the
-    context in which outputs and workspaces are made and the call is issued:
-    that device's current stream, or `stream` (their memory then belongs to it)."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensors must be on a CUDA device")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors are on {dev} and {t.device}")
-    if stream is None:
-        return torch.cuda.device(dev)
-    if stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-    return torch.cuda.stream(stream)
-
-
-def _expect(name, t, dtype, shape):
-    """t (None passes) has this dtype and shape."""
-    if t is None:
-        return
-    if t.dtype != dtype:
-        raise TypeError(f"{name} is {t.dtype}: expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} is {tuple(t.shape)}: expected {tuple(shape)}")
-
-
-def _norm_shape(x, groups, act, eps, scope):
+@functools.lru_cache(maxsize=4096)
+def _norm_plan(batch, seqlen, channels, groups, dtype, act, eps, backward, packed):
+    """(m3_norm_shape by reference, workspace bytes) of a call."""
     if act not in _ACTS:
         raise ValueError(f"act is {act!r}: expected one of {sorted(_ACTS)}")
-    C = x.shape[-1]
-    if scope == "token":
-        batch, seqlen = (x.numel() // C if C else 0), 1
-        if batch == 0:  # no token: one sample without positions
-            batch, seqlen = 1, 0
-    elif scope == "sequence":
-        if x.dim() != 3:
-            raise ValueError("scope 'sequence' takes x [batch][seqlen][channels]")
-        batch, seqlen = x.shape[0], x.shape[1]
-    else:
-        raise ValueError(f"scope is {scope!r}: expected 'token' or 'sequence'")
-    return NormShape(batch, seqlen, C, groups, _io_code(x.dtype), _ACTS[act], eps)
-
-
-def _norm_args(x, groups, weight, bias, z, act):
-    if groups < 1 or x.dim() < 1 or x.shape[-1] % groups != 0:
-        raise ValueError(f"{tuple(x.shape)} channels last do not split into {groups} groups")
-    C = x.shape[-1]
-    _expect("weight", weight, torch.float32, (C,))
-    _expect("bias", bias, torch.float32, (C,))
-    _expect("z", z, x.dtype, x.shape)
-    if (z is not None) != (act == "gate"):
-        raise ValueError("z belongs to act 'gate', and only to it")
-
-
-def _norm_workspace(shape, backward, packed, workspace, device):
+    shape = NormShape(batch, seqlen, channels, groups, _io_code(dtype), _ACTS[act], eps)
     n = ctypes.c_size_t(0)
     _check("m3_group_norm_workspace_size", load().m3_group_norm_workspace_size(
         ctypes.byref(shape), int(backward), int(packed), ctypes.byref(n)))
-    if workspace is None and n.value:
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=device)
-    return workspace, ctypes.c_size_t(0 if workspace is None else
-                                      workspace.numel() * workspace.element_size())
+    return ctypes.byref(shape), n.value
 
 
-def _norm_forward(name, shape, packed, x, weight, bias, z, y, workspace, stream, cu=None):
-    with _on(stream, x, weight, bias, z, y, workspace, cu):
-        if y is None:
-            y = torch.empty_like(x)
-        _expect("y", y, x.dtype, x.shape)
-        stat = (shape.batch if shape.seqlen or packed else 0, shape.groups)
-        mean = torch.empty(stat, dtype=torch.float32, device=x.device)
-        rstd = torch.empty(stat, dtype=torch.float32, device=x.device)
-        workspace, nbytes = _norm_workspace(shape, False, packed, workspace, x.device)
-        pre = [_ptr(cu), ctypes.c_int64(x.shape[0])] if packed else []
-        st = getattr(load(), name)(ctypes.byref(shape), *pre, _ptr(x), _ptr(weight), _ptr(bias),
-                                   _ptr(z), _ptr(y), _ptr(mean) if mean.numel() else None,
-                                   _ptr(rstd) if rstd.numel() else None, _ptr(workspace), nbytes,
-                                   _stream(stream))
-        _check(name, st)
-    return y, mean, rstd
+def _norm_extent(x, groups, scope):
+    """(samples, positions of each) of x [..][C]."""
+    C = x.shape[-1] if x.dim() else 0
+    if groups < 1 or C < 1 or C % groups != 0:
+        raise ValueError(f"{tuple(x.shape)} channels last do not split into {groups} groups")
+    if scope == "token":
+        return x.numel() // C, 1
+    if scope == "sequence":
+        if x.dim() != 3:
+            raise ValueError("scope 'sequence' takes x [batch][seqlen][channels]")
+        return x.shape[0], x.shape[1]
+    raise ValueError(f"scope is {scope!r}: expected 'token' or 'sequence'")
 
 
-def _norm_backward(name, shape, packed, x, mean, rstd, dy, weight, bias, z, workspace, stream,
-                   cu=None):
-    stat = (shape.batch if shape.seqlen or packed else 0, shape.groups)
-    _expect("mean", mean, torch.float32, stat)
-    _expect("rstd", rstd, torch.float32, stat)
-    _expect("dy", dy, x.dtype, x.shape)
-    C, f32 = x.shape[-1], torch.float32
-    with _on(stream, x, mean, rstd, dy, weight, bias, z, workspace, cu):
-        g = {"x": torch.empty_like(x), "weight": torch.empty((C,), dtype=f32, device=x.device),
-             "bias": torch.empty((C,), dtype=f32, device=x.device)}
+def _norm_call(name, plan, packed, x, groups, stat, weight, bias, z, act, y, dy, mean, rstd,
+               workspace, stream, cu=None):
+    """Forward (dy None) or backward call; returns its outputs."""
+    backward = dy is not None
+    dev = _device_of(x)
+    C, f32, dt, shape = x.shape[-1], torch.float32, x.dtype, x.shape
+    if (z is not None) != (act == "gate"):
+        raise ValueError("z belongs to act 'gate', and only to it")
+    px = _addr("x", x, dt, shape, dev)
+    pw, pb = _addr("weight", weight, f32, (C,), dev), _addr("bias", bias, f32, (C,), dev)
+    pz = _addr("z", z, dt, shape, dev)
+    ref, need = plan
+    pre = (_addr("cu_seqlens", cu, torch.int32, cu.shape, dev), shape[0]) if packed else ()
+    ctx, st = _enter(stream, dev)
+
+    def forward_call():
+        out = torch.empty_like(x) if y is None else y
+        mu = torch.empty(stat, dtype=f32, device=dev)
+        inv = torch.empty(stat, dtype=f32, device=dev)
+        pws, nws, keep = _scratch(need, workspace, dev)
+        _check(name, getattr(load(), name)(
+            ref, *pre, px, pw, pb, pz, _addr("y", out, dt, shape, dev), mu.data_ptr() or None,
+            inv.data_ptr() or None, pws, nws, st))
+        return out, mu, inv
+
+    def backward_call():
+        pm, pr = _addr("mean", mean, f32, stat, dev), _addr("rstd", rstd, f32, stat, dev)
+        pdy = _addr("dy", dy, dt, shape, dev)
+        g = {"x": torch.empty_like(x), "weight": torch.empty((C,), dtype=f32, device=dev),
+             "bias": torch.empty((C,), dtype=f32, device=dev)}
         if z is not None:
-            g["z"] = torch.empty_like(z)
-        workspace, nbytes = _norm_workspace(shape, True, packed, workspace, x.device)
-        pre = [_ptr(cu), ctypes.c_int64(x.shape[0])] if packed else []
-        st = getattr(load(), name)(ctypes.byref(shape), *pre, _ptr(x), _ptr(weight), _ptr(bias),
-                                   _ptr(z), _ptr(mean) if mean.numel() else None,
-                                   _ptr(rstd) if rstd.numel() else None, _ptr(dy), _ptr(g["x"]),
-                                   _ptr(g["weight"]), _ptr(g["bias"]), _ptr(g.get("z")),
-                                   _ptr(workspace), nbytes, _stream(stream))
-        _check(name, st)
-    return g
+            g["z"] = torch.empty_like(x)
+        pws, nws, keep = _scratch(need, workspace, dev)
+        _check(name, getattr(load(), name)(
+            ref, *pre, px, pw, pb, pz, pm, pr, pdy, g["x"].data_ptr(), g["weight"].data_ptr(),
+            g["bias"].data_ptr(), g["z"].data_ptr() if z is not None else None, pws, nws, st))
+        return g
+
+    return _run_in(ctx, backward_call if backward else forward_call)
 
 
 def m3_group_norm_fwd(x, groups: int, weight=None, bias=None, z=None, *, act="none",
@@ -663,35 +681,40 @@ def m3_group_norm_fwd(x, groups: int, weight=None, bias=None, z=None, *, act="no
     over all positions of a sequence too (scope "sequence", x [b][L][C]).
     act "none", "silu", or "gate" (times silu(z), z like x); weight, bias [C]
     fp32 or None.  Returns (y, mean, rstd), the statistics [samples][groups]."""
-    _norm_args(x, groups, weight, bias, z, act)
-    shape = _norm_shape(x, groups, act, eps, scope)
-    return _norm_forward("m3_group_norm_fwd", shape, False, x, weight, bias, z, y, workspace,
-                         stream)
+    batch, seqlen = _norm_extent(x, groups, scope)
+    stat = (batch, groups)
+    if batch == 0:  # no sample: to the library, one without positions
+        batch, seqlen = 1, 0
+    plan = _norm_plan(batch, seqlen, x.shape[-1], groups, x.dtype, act, eps, False, False)
+    return _norm_call("m3_group_norm_fwd", plan, False, x, groups, stat, weight, bias, z, act, y,
+                      None, None, None, workspace, stream)
 
 
 def m3_group_norm_bwd(x, groups: int, mean, rstd, dy, weight=None, bias=None, z=None, *,
                       act="none", scope="token", workspace=None, stream=None):
     """Backward of m3_group_norm_fwd from its inputs and statistics: a dict of
     x and (act "gate") z in the io dtype, weight and bias fp32 [C]."""
-    _norm_args(x, groups, weight, bias, z, act)
-    shape = _norm_shape(x, groups, act, 0.0, scope)
-    return _norm_backward("m3_group_norm_bwd", shape, False, x, mean, rstd, dy, weight, bias, z,
-                          workspace, stream)
+    batch, seqlen = _norm_extent(x, groups, scope)
+    stat = (batch, groups)
+    if batch == 0:  # no sample: to the library, one without positions
+        batch, seqlen = 1, 0
+    plan = _norm_plan(batch, seqlen, x.shape[-1], groups, x.dtype, act, 0.0, True, False)
+    return _norm_call("m3_group_norm_bwd", plan, False, x, groups, stat, weight, bias, z, act,
+                      None, dy, mean, rstd, workspace, stream)
 
 
-def _norm_packed_shape(cu_seqlens, x, groups, act, eps, max_seqlen):
+def _norm_packed(cu_seqlens, x, groups, max_seqlen):
     if cu_seqlens.dtype != torch.int32:
         raise TypeError("cu_seqlens must be int32")
     if x.dim() != 2:
         raise ValueError("a packed batch is x [tokens][channels]")
+    _norm_extent(x, groups, "token")
     S = cu_seqlens.numel() - 1
-    if S < 1:
+    if cu_seqlens.dim() != 1 or S < 1:
         raise ValueError("cu_seqlens holds no sequence")
     if max_seqlen is None:
         max_seqlen = int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item())
-    if act not in _ACTS:
-        raise ValueError(f"act is {act!r}: expected one of {sorted(_ACTS)}")
-    return NormShape(S, max_seqlen, x.shape[1], groups, _io_code(x.dtype), _ACTS[act], eps)
+    return S, max_seqlen
 
 
 def m3_group_norm_fwd_varlen(cu_seqlens, x, groups: int, weight=None, bias=None, z=None, *,
@@ -700,60 +723,60 @@ def m3_group_norm_fwd_varlen(cu_seqlens, x, groups: int, weight=None, bias=None,
     """m3_group_norm_fwd over the sequences of a packed batch: x [T][C],
     cu_seqlens [S+1] int32 on the device; max_seqlen as m3_scan_fwd_varlen.
     Rows of y outside every sequence are left as they are."""
-    _norm_args(x, groups, weight, bias, z, act)
-    shape = _norm_packed_shape(cu_seqlens, x, groups, act, eps, max_seqlen)
-    return _norm_forward("m3_group_norm_fwd_varlen", shape, True, x, weight, bias, z, y,
-                         workspace, stream, cu_seqlens)
+    S, L = _norm_packed(cu_seqlens, x, groups, max_seqlen)
+    plan = _norm_plan(S, L, x.shape[1], groups, x.dtype, act, eps, False, True)
+    return _norm_call("m3_group_norm_fwd_varlen", plan, True, x, groups, (S, groups), weight,
+                      bias, z, act, y, None, None, None, workspace, stream, cu_seqlens)
 
 
 def m3_group_norm_bwd_varlen(cu_seqlens, x, groups: int, mean, rstd, dy, weight=None, bias=None,
                              z=None, *, act="none", max_seqlen=None, workspace=None, stream=None):
     """Backward of m3_group_norm_fwd_varlen (the dict of m3_group_norm_bwd);
     rows of dx and dz outside every sequence are undefined."""
-    _norm_args(x, groups, weight, bias, z, act)
-    shape = _norm_packed_shape(cu_seqlens, x, groups, act, 0.0, max_seqlen)
-    return _norm_backward("m3_group_norm_bwd_varlen", shape, True, x, mean, rstd, dy, weight,
-                          bias, z, workspace, stream, cu_seqlens)
+    S, L = _norm_packed(cu_seqlens, x, groups, max_seqlen)
+    plan = _norm_plan(S, L, x.shape[1], groups, x.dtype, act, 0.0, True, True)
+    return _norm_call("m3_group_norm_bwd_varlen", plan, True, x, groups, (S, groups), weight,
+                      bias, z, act, None, dy, mean, rstd, workspace, stream, cu_seqlens)
 
 
 # ---- the head's cross entropy ---------------------------------------------------
 
 def _xent_args(h, W, targets):
-    if h.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
-        raise TypeError("the head takes bf16 h and W")
-    if targets.dtype != torch.int64:
-        raise TypeError(f"targets is {targets.dtype}: expected {torch.int64}")
+    """(tokens, vocabulary, width, device) and the addresses of the three."""
+    bf16 = torch.bfloat16
     if W.dim() != 2 or h.dim() < 1 or h.shape[-1] != W.shape[1]:
         raise ValueError(f"h is {tuple(h.shape)} and W {tuple(W.shape)}: expected [..][K], [V][K]")
-    if targets.shape != h.shape[:-1]:
-        raise ValueError(f"targets is {tuple(targets.shape)}: expected {tuple(h.shape[:-1])}")
-    return targets.numel(), W.shape[0], W.shape[1]
+    dev = _device_of(h)
+    V, K = W.shape
+    ptrs = (_addr("h", h, bf16, h.shape, dev), _addr("W", W, bf16, W.shape, dev),
+            _addr("targets", targets, torch.int64, h.shape[:-1], dev))
+    return (targets.numel(), V, K), dev, ptrs
 
 
-def _xent_workspace(name, sizes, workspace, device):
+@functools.lru_cache(maxsize=4096)
+def _xent_bytes(name, sizes):
     n = ctypes.c_size_t(0)
     _check(name, getattr(load(), name)(*sizes, ctypes.byref(n)))
-    if workspace is None and n.value:
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=device)
-    return workspace, ctypes.c_size_t(0 if workspace is None else
-                                      workspace.numel() * workspace.element_size())
+    return n.value
 
 
 def m3_linear_xent_fwd(h, W, targets, *, ignore_index: int = -100, workspace=None, stream=None):
     """Softmax cross entropy of logits = h W^T, which are never stored: h [..][K]
     bf16, W [V][K] bf16, targets [..] int64 (ignore_index: not scored).  Returns
     (loss, lse), fp32 and shaped like targets."""
-    sizes = [ctypes.c_int64(v) for v in _xent_args(h, W, targets)]
-    with _on(stream, h, W, targets, workspace):
-        loss = torch.empty(targets.shape, dtype=torch.float32, device=h.device)
-        lse = torch.empty(targets.shape, dtype=torch.float32, device=h.device)
-        workspace, nbytes = _xent_workspace("m3_linear_xent_fwd_workspace_size", sizes, workspace,
-                                            h.device)
-        st = load().m3_linear_xent_fwd(*sizes, _ptr(h), _ptr(W), _ptr(targets),
-                                       ctypes.c_int64(ignore_index), _ptr(loss), _ptr(lse),
-                                       _ptr(workspace), nbytes, _stream(stream))
-        _check("m3_linear_xent_fwd", st)
-    return loss, lse
+    sizes, dev, ptrs = _xent_args(h, W, targets)
+    need = _xent_bytes("m3_linear_xent_fwd_workspace_size", sizes)
+    ctx, st = _enter(stream, dev)
+
+    def call():
+        loss = torch.empty(targets.shape, dtype=torch.float32, device=dev)
+        lse = torch.empty(targets.shape, dtype=torch.float32, device=dev)
+        pws, nws, keep = _scratch(need, workspace, dev)
+        _check("m3_linear_xent_fwd", load().m3_linear_xent_fwd(
+            *sizes, *ptrs, ignore_index, loss.data_ptr(), lse.data_ptr(), pws, nws, st))
+        return loss, lse
+
+    return _run_in(ctx, call)
 
 
 def m3_linear_xent_bwd(h, W, targets, lse, dloss, *, ignore_index: int = -100, want_dh=True,
@@ -761,20 +784,22 @@ def m3_linear_xent_bwd(h, W, targets, lse, dloss, *, ignore_index: int = -100, w
     """Backward of m3_linear_xent_fwd: (dh, dW) bf16, the gradients of
     sum(loss * dloss) (None for one that is not wanted).  lse as the forward
     gave it, dloss fp32 shaped like targets."""
-    sizes = [ctypes.c_int64(v) for v in _xent_args(h, W, targets)]
-    _expect("lse", lse, torch.float32, targets.shape)
-    _expect("dloss", dloss, torch.float32, targets.shape)
-    with _on(stream, h, W, targets, lse, dloss, workspace):
+    sizes, dev, ptrs = _xent_args(h, W, targets)
+    plse = _addr("lse", lse, torch.float32, targets.shape, dev)
+    pdl = _addr("dloss", dloss, torch.float32, targets.shape, dev)
+    need = _xent_bytes("m3_linear_xent_bwd_workspace_size", sizes)
+    ctx, st = _enter(stream, dev)
+
+    def call():
         dh = torch.empty_like(h) if want_dh else None
         dW = torch.empty_like(W) if want_dW else None
-        workspace, nbytes = _xent_workspace("m3_linear_xent_bwd_workspace_size", sizes, workspace,
-                                            h.device)
-        st = load().m3_linear_xent_bwd(*sizes, _ptr(h), _ptr(W), _ptr(targets),
-                                       ctypes.c_int64(ignore_index), _ptr(lse), _ptr(dloss),
-                                       _ptr(dh), _ptr(dW), _ptr(workspace), nbytes,
-                                       _stream(stream))
-        _check("m3_linear_xent_bwd", st)
-    return dh, dW
+        pws, nws, keep = _scratch(need, workspace, dev)
+        _check("m3_linear_xent_bwd", load().m3_linear_xent_bwd(
+            *sizes, *ptrs, ignore_index, plse, pdl, dh.data_ptr() if want_dh else None,
+            dW.data_ptr() if want_dW else None, pws, nws, st))
+        return dh, dW
+
+    return _run_in(ctx, call)
 
 
 # ---- 4-bit weights ---------------------------------------------------------------
@@ -788,16 +813,20 @@ def m3_w4_quantize(W, group: int = 128, *, symmetric=False, stream=None):
     N, K = W.shape
     if group not in (32, 64, 128) or K % group != 0 or K == 0:
         raise ValueError(f"{K} inputs do not split into groups of {group} (32, 64 or 128)")
-    with _on(stream, W):
-        codes = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
-        scales = torch.empty((N, K // group), dtype=torch.bfloat16, device=W.device)
-        zeros = None if symmetric else torch.empty((N, K // group), dtype=torch.uint8,
-                                                   device=W.device)
-        st = load().m3_w4_quantize(ctypes.c_int64(N), ctypes.c_int64(K), ctypes.c_int32(group),
-                                   ctypes.c_int32(_io_code(W.dtype)), _ptr(W), _ptr(codes),
-                                   _ptr(scales), _ptr(zeros), _stream(stream))
-        _check("m3_w4_quantize", st)
-    return codes, scales, zeros
+    dev = _device_of(W)
+    code, pW = _io_code(W.dtype), _addr("W", W, W.dtype, W.shape, dev)
+    ctx, st = _enter(stream, dev)
+
+    def call():
+        codes = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
+        scales = torch.empty((N, K // group), dtype=torch.bfloat16, device=dev)
+        zeros = None if symmetric else torch.empty((N, K // group), dtype=torch.uint8, device=dev)
+        _check("m3_w4_quantize", load().m3_w4_quantize(
+            N, K, group, code, pW, codes.data_ptr(), scales.data_ptr(),
+            None if symmetric else zeros.data_ptr(), st))
+        return codes, scales, zeros
+
+    return _run_in(ctx, call)
 
 
 def m3_linear_w4(A, codes, scales, zeros=None, bias=None, *, out=None, out_dtype=torch.bfloat16,
@@ -806,29 +835,29 @@ def m3_linear_w4(A, codes, scales, zeros=None, bias=None, *, out=None, out_dtype
     A [..][K] bf16, codes [N][K/2] uint8, scales [N][K/group] bf16, zeros
     [N][K/group] uint8 or None (8); returns out [..][N] in out_dtype (bf16 or
     fp32)."""
-    if A.dtype != torch.bfloat16:
-        raise TypeError(f"A is {A.dtype}: expected {torch.bfloat16}")
     if codes.dim() != 2 or scales.dim() != 2:
         raise ValueError("codes and scales are [N][..]")
     N, K = codes.shape[0], 2 * codes.shape[1]
-    _expect("codes", codes, torch.uint8, (N, K // 2))
     if A.dim() < 1 or A.shape[-1] != K:
         raise ValueError(f"A is {tuple(A.shape)}: expected [..][{K}]")
-    if scales.shape[1] == 0 or K % scales.shape[1] != 0:
+    ng = scales.shape[1]
+    if ng == 0 or K % ng != 0:
         raise ValueError(f"scales is {tuple(scales.shape)} for {K} inputs")
-    _expect("scales", scales, torch.bfloat16, (N, scales.shape[1]))
-    _expect("zeros", zeros, torch.uint8, scales.shape)
-    _expect("bias", bias, torch.float32, (N,))
+    dev, bf16, u8 = _device_of(A), torch.bfloat16, torch.uint8
     if out is not None:
         out_dtype = out.dtype
     code = _io_code(out_dtype)
-    with _on(stream, A, codes, scales, zeros, bias, out):
-        if out is None:
-            out = torch.empty(A.shape[:-1] + (N,), dtype=out_dtype, device=A.device)
-        _expect("out", out, out_dtype, A.shape[:-1] + (N,))
-        st = load().m3_linear_w4(ctypes.c_int64(A.numel() // K), ctypes.c_int64(N),
-                                 ctypes.c_int64(K), ctypes.c_int32(K // scales.shape[1]), _ptr(A),
-                                 _ptr(codes), _ptr(scales), _ptr(zeros), _ptr(bias), _ptr(out),
-                                 ctypes.c_int32(code), _stream(stream))
-        _check("m3_linear_w4", st)
-    return out
+    pA, pc = _addr("A", A, bf16, A.shape, dev), _addr("codes", codes, u8, codes.shape, dev)
+    ps = _addr("scales", scales, bf16, (N, ng), dev)
+    pz, pb = _addr("zeros", zeros, u8, (N, ng), dev), _addr("bias", bias, torch.float32, (N,), dev)
+    full = A.shape[:-1] + (N,)
+    ctx, st = _enter(stream, dev)
+
+    def call():
+        o = torch.empty(full, dtype=out_dtype, device=dev) if out is None else out
+        _check("m3_linear_w4", load().m3_linear_w4(
+            A.numel() // K, N, K, K // ng, pA, pc, ps, pz, pb, _addr("out", o, out_dtype, full, dev),
+            code, st))
+        return o
+
+    return _run_in(ctx, call)
