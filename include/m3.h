@@ -483,7 +483,7 @@ M3_API int m3_linear_xent_bwd(int64_t tokens, int64_t vocab, int64_t width, cons
  *               (+ bias[n]),
  * fp32 sums of exact products; the weights are never rounded to bf16.
  *   M >= 0 tokens, N >= 1 outputs, K >= group inputs, K % group == 0,
- *   group 32, 64 or 128; M, N, K < 2^31 - 256.
+ *   group 32, 64 or 128; M, N, K < 2^30.
  *   A        [M][K] bf16;  out [M][N], out_dtype M3_BF16 or M3_F32.
  *   codes    [N][K/2]: two codes q in 0..15 a byte, input 2j in the low half
  *            of byte j.

@@ -8,9 +8,10 @@
 // bf16, so a group's sum on the tensor cores (mma m16n8k16, fp32 accumulation)
 // loses nothing to rounded weights, and its scale is applied to the fp32 sum.
 //
-// A producer thread streams the codes by TMA, in boxes of 256 inputs (128
-// bytes, swizzled) x 16 MT outputs, one box for each of eight warps in a stage.
-// A warp turns its box into the product's A operand in registers: which input a
+// Each of sixteen warps streams its own codes by TMA, in boxes of 256 inputs (128
+// bytes, swizzled) x 16 MT outputs through a ring of its own, and refills a slot
+// when it has read it: the warps meet only where their parts of the inputs are
+// added.  A warp turns its box into the product's A operand in registers: which input a
 // fragment's slot stands for is free as long as both operands agree, so each
 // lane takes the consecutive inputs of one wide shared-memory load, and the
 // tokens' values are laid out once per block in that order.  A word of eight
@@ -30,11 +31,12 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWarps = 8;               // consumers; one more warp produces
-constexpr int kThreads = 32 * kWarps + 32;
+constexpr int kWarps = 16;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kBox = 256;               // inputs of a box: 128 bytes of codes
 constexpr int kXChunk = 4 * 32 * 16;    // bytes of eight tokens' values of 128 inputs
-constexpr int kMostStages = 8;
+constexpr int kMostStages = 8;         // of a warp's ring
+constexpr int kSmemMost = 226 * 1024;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -45,10 +47,26 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The first product of a group: no accumulator to clear.
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
                                    *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// (v & mask) | magic as one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(magic));
+  return r;
 }
 
 __device__ bool w4_wait(uint64_t* bar, uint32_t parity, int* status) {
@@ -89,51 +107,57 @@ struct Params {
   uint32_t z[2][(NG + 3) / 4];  // bytes
 };
 
-template <int G, bool ZEROS>
-__device__ __forceinline__ void load_params(const W4Args& a, bool vec, int64_t row0, int64_t k0,
-                                            int lane, Params<G>& o) {
+// s, z: the lane's place in the first of its rows, at the box's first group;
+// kg8: eight rows on.  rows, cols: how many rows and groups there are from here.
+template <int G, bool ZEROS, int MT>
+__device__ __forceinline__ void load_params(const uint16_t* s, const uint8_t* z, int64_t kg8,
+                                            bool vec, int rows, int cols,
+                                            Params<G> (&o)[MT]) {
   constexpr int NG = Params<G>::NG;
-  const int64_t kg = a.K / G;
+  if (vec && rows > 16 * MT - 8 && cols > 0) {  // whole rows, aligned pieces
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t row = row0 + output_of<G>(lane >> 2) + 8 * h;
-    const int64_t at = row * kg + k0 / G;
+    for (int t = 0; t < MT; ++t) {
 #pragma unroll
-    for (int i = 0; i < (NG + 1) / 2; ++i) o.s[h][i] = 0;
-#pragma unroll
-    for (int i = 0; i < (NG + 3) / 4; ++i) o.z[h][i] = 0x08080808u;
-    if (row >= a.N || k0 >= a.K) continue;
-    const uint16_t* s = static_cast<const uint16_t*>(a.scales) + at;
-    const uint8_t* z = a.zeros + at;
-    if (vec) {  // K is a multiple of 256: a row's box is whole and aligned
-      if constexpr (NG == 8) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(s));
-        o.s[h][0] = v.x; o.s[h][1] = v.y; o.s[h][2] = v.z; o.s[h][3] = v.w;
-      } else if constexpr (NG == 4) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(s));
-        o.s[h][0] = v.x; o.s[h][1] = v.y;
-      } else {
-        o.s[h][0] = __ldg(reinterpret_cast<const uint32_t*>(s));
-      }
-      if constexpr (ZEROS) {
+      for (int h = 0; h < 2; ++h, s += kg8, z += kg8) {
+        Params<G>& p = o[t];
         if constexpr (NG == 8) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(z));
-          o.z[h][0] = v.x; o.z[h][1] = v.y;
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(s));
+          p.s[h][0] = v.x; p.s[h][1] = v.y; p.s[h][2] = v.z; p.s[h][3] = v.w;
         } else if constexpr (NG == 4) {
-          o.z[h][0] = __ldg(reinterpret_cast<const uint32_t*>(z));
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(s));
+          p.s[h][0] = v.x; p.s[h][1] = v.y;
         } else {
-          o.z[h][0] = __ldg(reinterpret_cast<const uint16_t*>(z));
+          p.s[h][0] = __ldg(reinterpret_cast<const uint32_t*>(s));
+        }
+        if constexpr (ZEROS) {
+          if constexpr (NG == 8) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(z));
+            p.z[h][0] = v.x; p.z[h][1] = v.y;
+          } else if constexpr (NG == 4) {
+            p.z[h][0] = __ldg(reinterpret_cast<const uint32_t*>(z));
+          } else {
+            p.z[h][0] = __ldg(reinterpret_cast<const uint16_t*>(z));
+          }
         }
       }
-    } else {
+    }
+    return;
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h, s += kg8, z += kg8) {
+      Params<G>& p = o[t];
+#pragma unroll
+      for (int i = 0; i < (NG + 1) / 2; ++i) p.s[h][i] = 0;
+#pragma unroll
+      for (int i = 0; i < (NG + 3) / 4; ++i) p.z[h][i] = 0;
+      if (t * 16 + h * 8 >= rows) continue;
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        if (k0 + i * G >= a.K) continue;
-        o.s[h][i / 2] |= (uint32_t)__ldg(s + i) << (16 * (i & 1));
-        if constexpr (ZEROS) {
-          const int sh = 8 * (i & 3);
-          o.z[h][i / 4] = (o.z[h][i / 4] & ~(0xffu << sh)) | ((uint32_t)__ldg(z + i) << sh);
-        }
+        if (i >= cols) continue;
+        p.s[h][i / 2] |= (uint32_t)__ldg(s + i) << (16 * (i & 1));
+        if constexpr (ZEROS) p.z[h][i / 4] |= (uint32_t)__ldg(z + i) << (8 * (i & 3));
       }
     }
   }
@@ -144,10 +168,23 @@ __device__ __forceinline__ void load_params(const W4Args& a, bool vec, int64_t r
 // tokens' values of the box's two chunks.
 template <int G, bool ZEROS, int MT, int NT>
 __device__ __forceinline__ void box_products(const uint8_t* codes, const uint8_t* xs, int xstride,
-                                             const Params<G> (&pr)[MT], int lane,
-                                             float (&acc)[MT][NT][4]) {
+                                             const Params<G> (&pr)[MT], int lane, uint32_t mask,
+                                             uint32_t magic, float (&acc)[MT][NT][4]) {
   constexpr int words = G / 32, NG = kBox / G;
   const int r = output_of<G>(lane >> 2), c = lane & 3;
+  // a lane's piece of group i: byte i * G / 2 + c * G / 8 of its row, the 16-byte
+  // pieces swizzled by the row (r + 8 swizzles as r)
+  const uint8_t* row = codes + r * 128 + ((c * (G / 8)) & 15);
+  const uint32_t piece = (uint32_t)(((c * (G / 8)) & ~15) ^ (r << 4));
+  uint32_t zb[MT][2][(NG + 3) / 4];
+  if constexpr (ZEROS) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < (NG + 3) / 4; ++i) zb[t][h][i] = pr[t].z[h][i] & 0x0f0f0f0fu;
+  }
 #pragma unroll
   for (int i = 0; i < NG; ++i) {
     const int ch = i * G / 128, in = (i * G % 128) / 32;  // chunk, first word of the group in it
@@ -156,9 +193,7 @@ __device__ __forceinline__ void box_products(const uint8_t* codes, const uint8_t
     for (int t = 0; t < MT; ++t) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint8_t* row = codes + (t * 16 + r + 8 * h) * 128;
-        const int byte = i * (G / 2) + c * (G / 8);
-        const uint8_t* p = row + ((((byte >> 4) ^ r) << 4) | (byte & 15));  // r + 8 swizzles as r
+        const uint8_t* p = row + (t * 16 + 8 * h) * 128 + (piece ^ (uint32_t)(i * (G / 2)));
         if constexpr (G == 128) {
           const uint4 v = *reinterpret_cast<const uint4*>(p);
           q[t][h][0] = v.x; q[t][h][1] = v.y; q[t][h][2] = v.z; q[t][h][3] = v.w;
@@ -168,15 +203,12 @@ __device__ __forceinline__ void box_products(const uint8_t* codes, const uint8_t
         } else {
           q[t][h][0] = *reinterpret_cast<const uint32_t*>(p);
         }
-        zz[t][h] = ZEROS ? 0x43004300u + ((pr[t].z[h][i / 4] >> (8 * (i & 3))) & 15u) * 0x00010001u
+        // 128 + z, twice: the zero point's byte below 0x43
+        zz[t][h] = ZEROS ? __byte_perm(zb[t][h][i / 4], 0x43434343u, 0x4040u | ((i & 3) * 0x0101u))
                          : 0x43084308u;
       }
     }
     float d[MT][NT][4];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) d[t][n][0] = d[t][n][1] = d[t][n][2] = d[t][n][3] = 0.f;
 #pragma unroll
     for (int w = 0; w < words; ++w) {
       uint32_t a0[MT][4], a1[MT][4];
@@ -187,7 +219,7 @@ __device__ __forceinline__ void box_products(const uint8_t* codes, const uint8_t
           uint32_t f[4];  // pairs (e, e + 4), e = 0..3
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            f[e] = sub_bf16x2(((q[t][h][w] >> (4 * e)) & 0x000f000fu) | 0x43004300u, zz[t][h]);
+            f[e] = sub_bf16x2(and_or(q[t][h][w] >> (4 * e), mask, magic), zz[t][h]);
           a0[t][h] = f[0]; a0[t][2 + h] = f[1];
           a1[t][h] = f[2]; a1[t][2 + h] = f[3];
         }
@@ -198,7 +230,10 @@ __device__ __forceinline__ void box_products(const uint8_t* codes, const uint8_t
                                                         ((in + w) * 32 + lane) * 16);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-          mma_bf16(d[t][n], a0[t], b.x, b.y);
+          if (w == 0)
+            mma_bf16_first(d[t][n], a0[t], b.x, b.y);
+          else
+            mma_bf16(d[t][n], a0[t], b.x, b.y);
           mma_bf16(d[t][n], a1[t], b.z, b.w);
         }
       }
@@ -224,7 +259,7 @@ template <int G, int NT>
 __device__ __forceinline__ void stage_tokens(const W4Args& a, uint8_t* xs, int64_t m0,
                                              int64_t box0, int boxes) {
   const int n = 2 * boxes;
-  for (int i = threadIdx.x; i < NT * n * 128; i += 32 * kWarps) {
+  for (int i = threadIdx.x; i < NT * n * 128; i += kThreads) {
     const int lane = i & 31, w = (i >> 5) & 3;
     const int ch = (i >> 7) % n, t = (i >> 7) / n;
     const int64_t m = m0 + t * 8 + (lane >> 2);
@@ -242,155 +277,150 @@ __device__ __forceinline__ void stage_tokens(const W4Args& a, uint8_t* xs, int64
 }
 
 struct W4Plan {
-  int boxes;    // boxes of a row in one stage (at most a warp each)
-  int slices;   // stages of a row's inputs
-  int rb;       // row blocks of 16 MT outputs in a stage
-  int stages;
-  int xboxes;   // boxes whose token values are held: all of a row's, or one slice's
-  int64_t items;  // groups of rb row blocks
+  int ks;       // warps that share a row block's inputs, box by box in turn
+  int slices;   // boxes of each of them
+  int rb;       // row blocks of 16 MT outputs in an item
+  int stages;   // boxes of a warp's ring
+  int xboxes;   // boxes whose token values are held: all of a row's, or ks
+  int items;    // groups of rb row blocks
+  int all;      // boxes of a row
+  // 0x000f000f and 0x43004300: as kernel arguments they are operands from the
+  // constant bank; as literals each use first moved one into a register
+  uint32_t mask, magic;
 };
 
-__device__ __forceinline__ void consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
-}
-
 template <int G, bool ZEROS, int MT, int NT>
-__global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, 1)
 w4_kernel(const W4Args a, const W4Plan p, const __grid_constant__ CUtensorMap map) {
   extern __shared__ __align__(1024) uint8_t sm[];
   constexpr int kBoxBytes = 16 * MT * 128;
   constexpr int kRed = 16 * MT * 8 * NT;  // a warp's partial sums
-  constexpr int kRedBufs = NT == 1 ? 2 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nbox = p.boxes * p.rb;
-  const int stage_bytes = nbox * kBoxBytes;
-  uint8_t* xs = sm + p.stages * stage_bytes;
-  float* red = reinterpret_cast<float*>(xs + (size_t)NT * p.xboxes * 2 * kXChunk);  // [bufs][warp][kRed]
-  uint64_t* full = reinterpret_cast<uint64_t*>(red + kRedBufs * kWarps * kRed);
-  uint64_t* empty = full + kMostStages;
+  uint8_t* ring = sm + warp * p.stages * kBoxBytes;
+  uint8_t* xs = sm + kWarps * p.stages * kBoxBytes;
+  float* red = reinterpret_cast<float*>(xs + (size_t)NT * p.xboxes * 2 * kXChunk);  // [warp][kRed]
+  uint64_t* full = reinterpret_cast<uint64_t*>(red + kWarps * kRed) + warp * kMostStages;
   if ((smem_u32(sm) & 1023u) != 0) {  // the swizzled boxes need 1 KB alignment
     if (threadIdx.x == 0 && a.status) atomicCAS(a.status, 0, (int)M3_ERR_CUDA);
     return;
   }
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kWarps);
-    }
-    fence_mbar_init();
-  }
-  __syncthreads();
-
-  if (warp == kWarps) {
-    if (lane != 0) return;
-    uint32_t it = 0;
-    bool ok = true;
-    for (int64_t item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
-      for (int sl = 0; sl < p.slices; ++sl, ++it) {
-        const int s = (int)(it % (uint32_t)p.stages);
-        ok = w4_wait(&empty[s], ((it / (uint32_t)p.stages) & 1u) ^ 1u, a.status);
-        if (!ok) break;
-        mbar_expect_tx(&full[s], (uint32_t)stage_bytes);
-        for (int b = 0; b < nbox; ++b) {
-          const int64_t row = (item * p.rb + b / p.boxes) * 16 * MT;
-          const int64_t box = (int64_t)sl * p.boxes + b % p.boxes;
-          asm volatile(
-              "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
-              "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(sm + s * stage_bytes + b * kBoxBytes)),
-              "l"(reinterpret_cast<uint64_t>(&map)), "r"((int)(box * (kBox / 2))), "r"((int)row),
-              "r"(smem_u32(&full[s]))
-              : "memory");
-        }
-      }
-    }
-    // let the last stages' copies land (bounded) before the block can exit
-    const uint32_t st = (uint32_t)p.stages;
-    for (uint32_t j = it > st ? it - st : 0; j < it; ++j)
-      w4_wait(&full[j % st], (j / st) & 1u, a.status);
-    return;
-  }
-
   const int64_t m0 = (int64_t)blockIdx.y * 8 * NT;
   const bool vec = a.K % kBox == 0;
-  const int mybox = warp % p.boxes, myrb = warp / p.boxes;
-  const bool busy = warp < nbox;
-  const bool whole = p.slices == 1 || p.xboxes > p.boxes;  // all token values are held
+  const int part = warp % p.ks, myrb = warp / p.ks;
+  const bool busy = myrb < p.rb;
+  const int row_step = (int)gridDim.x * p.rb * 16 * MT;  // from an item to the block's next
+
+  // lane 0 keeps the ring full: the next box's row, slice and slot
+  int pitem = (int)blockIdx.x, prow = ((int)blockIdx.x * p.rb + myrb) * 16 * MT, psl = 0, pslot = 0;
+  auto ask = [&] {
+    if (pitem >= p.items) return;
+    mbar_expect_tx(&full[pslot], (uint32_t)kBoxBytes);
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(ring + pslot * kBoxBytes)),
+        "l"(reinterpret_cast<uint64_t>(&map)), "r"((psl * p.ks + part) * (kBox / 2)), "r"(prow),
+        "r"(smem_u32(&full[pslot]))
+        : "memory");
+    if (++pslot == p.stages) pslot = 0;
+    if (++psl == p.slices) {
+      psl = 0;
+      prow += row_step;
+      pitem += (int)gridDim.x;
+    }
+  };
+  if (busy && lane == 0) {
+    for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+    for (int s = 0; s < p.stages; ++s) ask();
+  }
+  __syncwarp();
+  const uint32_t magic = p.magic;
+  const bool whole = p.xboxes >= p.ks * p.slices;  // all token values are held
   if (whole) {
     stage_tokens<G, NT>(a, xs, m0, 0, p.xboxes);
-    consumers_sync();
+    __syncthreads();
   }
-  uint32_t it = 0, buf = 0;
+
+  // the lane's place in scales and zeros: its first row of the item, its box
+  const int kg = (int)(a.K / G);
+  int left = (int)a.N - (((int)blockIdx.x * p.rb + myrb) * 16 * MT + output_of<G>(lane >> 2));
+  int64_t at = ((int64_t)a.N - left) * kg + part * (kBox / G);
+  const int64_t to_item = (int64_t)row_step * kg - (int64_t)(p.slices - 1) * p.ks * (kBox / G);
+  const int to_slice = p.ks * (kBox / G);
+  auto params = [&](int box, Params<G>(&o)[MT]) {
+    load_params<G, ZEROS, MT>(static_cast<const uint16_t*>(a.scales) + at, a.zeros + at,
+                              8 * (int64_t)kg, vec, left, box < p.all ? kg - box * (kBox / G) : 0, o);
+  };
+  int slot = 0;
+  uint32_t phase = 0;
   bool ok = true;
   Params<G> pr[MT];
-  if (busy && blockIdx.x < p.items) {
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-      load_params<G, ZEROS>(a, vec, (((int64_t)blockIdx.x * p.rb + myrb) * MT + t) * 16,
-                            (int64_t)mybox * kBox, lane, pr[t]);
-  }
-  for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x, buf ^= 1u) {
+  if (busy) params(part, pr);
+  for (int item = (int)blockIdx.x; item < p.items; item += (int)gridDim.x) {
     float acc[MT][NT][4];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[t][n][0] = acc[t][n][1] = acc[t][n][2] = acc[t][n][3] = 0.f;
-    for (int sl = 0; sl < p.slices; ++sl, ++it) {
+    for (int sl = 0; sl < p.slices; ++sl) {
       if (!whole) {
-        consumers_sync();
-        stage_tokens<G, NT>(a, xs, m0, (int64_t)sl * p.boxes, p.xboxes);
-        consumers_sync();
+        __syncthreads();
+        stage_tokens<G, NT>(a, xs, m0, (int64_t)sl * p.ks, p.xboxes);
+        __syncthreads();
       }
-      const int s = (int)(it % (uint32_t)p.stages);
-      if (ok) ok = w4_wait(&full[s], (it / (uint32_t)p.stages) & 1u, a.status);
-      // the next stage's scales are on their way while this one is multiplied
+      if (!busy) continue;
+      if (ok) ok = __all_sync(0xffffffffu, w4_wait(&full[slot], phase, a.status));
+      // the next box's scales are on their way while this one is multiplied
       Params<G> nx[MT];
       const bool more = sl + 1 < p.slices;
-      const int64_t nitem = more ? item : item + gridDim.x;
-      if (busy && nitem < p.items) {
-        const int64_t nbx = (int64_t)(more ? sl + 1 : 0) * p.boxes + mybox;
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-          load_params<G, ZEROS>(a, vec, ((nitem * p.rb + myrb) * MT + t) * 16, nbx * kBox, lane,
-                                nx[t]);
+      at += more ? (int64_t)to_slice : to_item;
+      if (!more) left -= row_step;
+      params(more ? (sl + 1) * p.ks + part : part, nx);
+      if (ok) {
+        const int xb = whole ? sl * p.ks + part : part;
+        box_products<G, ZEROS, MT, NT>(ring + slot * kBoxBytes, xs + (size_t)xb * 2 * kXChunk,
+                                       p.xboxes * 2 * kXChunk, pr, lane, p.mask, magic, acc);
       }
-      if (busy && ok) {
-        const int64_t xb = whole ? (int64_t)sl * p.boxes + mybox : mybox;
-        if (xb < p.xboxes)
-          box_products<G, ZEROS, MT, NT>(sm + s * stage_bytes + warp * kBoxBytes,
-                                         xs + (size_t)xb * 2 * kXChunk, p.xboxes * 2 * kXChunk, pr,
-                                         lane, acc);
+      __syncwarp();  // every lane has read the slot
+      if (ok && lane == 0) ask();
+      if (ok && ++slot == p.stages) {
+        slot = 0;
+        phase ^= 1u;
       }
-      __syncwarp();
-      if (lane == 0)
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&empty[s])) : "memory");
 #pragma unroll
       for (int t = 0; t < MT; ++t) pr[t] = nx[t];
     }
-    // the warps' parts of the inputs, added in order; with two buffers one
-    // barrier an item is enough
-    if (kRedBufs == 1) consumers_sync();
-    float* r = red + (kRedBufs == 1 ? 0 : buf * kWarps * kRed);
+    // the warps' parts of the inputs, added in order
     if (busy) {
+      float* r = red + warp * kRed + output_of<G>(lane >> 2) + 16 * MT * 2 * (lane & 3);
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            r[warp * kRed + t * 16 + output_of<G>(lane >> 2) + (i >> 1) * 8 +
-              16 * MT * (n * 8 + (lane & 3) * 2 + (i & 1))] = acc[t][n][i];
+            r[t * 16 + (i >> 1) * 8 + 16 * MT * (n * 8 + (i & 1))] = acc[t][n][i];
     }
-    consumers_sync();
-    for (int i = threadIdx.x; i < p.rb * kRed; i += 32 * kWarps) {
-      const int st = i / kRed, at = i % kRed;
-      const int64_t n = (item * p.rb + st) * 16 * MT + at % (16 * MT), m = m0 + at / (16 * MT);
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.rb * kRed; i += kThreads) {
+      const int st = i / kRed, o = i % kRed;
+      const int64_t n = (item * p.rb + st) * 16 * MT + o % (16 * MT), m = m0 + o / (16 * MT);
       if (n >= a.N || m >= a.M) continue;
-      float v = r[st * p.boxes * kRed + at];
-      for (int k = 1; k < p.boxes; ++k) v += r[(st * p.boxes + k) * kRed + at];
+      const float* r = red + st * p.ks * kRed + o;
+      float v = r[0];
+      for (int k = 1; k < p.ks; ++k) v += r[k * kRed];
       if (a.bias) v += __ldg(a.bias + n);
       if (M3_IN(m * a.N + n, a.M * a.N, a.status)) io_store(a.out, m * a.N + n, v, !a.out_f32);
     }
+    if (item + (int)gridDim.x < p.items) __syncthreads();  // before the sums are overwritten
   }
+  // after a wait that gave up: the copies asked for land (bounded) before the
+  // block can exit; of a slot's copies only the last can still be out
+  if (busy && !ok && lane == 0)
+    for (int k = 0; k < p.stages; ++k) {
+      if (slot == k) continue;
+      w4_wait(&full[k], phase ^ (k < slot ? 1u : 0u), a.status);
+    }
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -425,27 +455,42 @@ bool encode_codes(CUtensorMap* m, const W4Args& a, int rows) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// How the work is cut for `MT` row tiles a warp and `NT` token tiles; false
+// where a ring of two boxes does not fit beside all of a row's token values.
+bool make_plan(const W4Args& a, int MT, int NT, bool whole, W4Plan* p) {
+  const int box = 16 * MT * 128, red = kWarps * 16 * MT * 8 * NT * 4;
+  const int64_t all = (a.K + kBox - 1) / kBox;  // boxes of a row
+  const int64_t rows = (a.N + 16 * MT - 1) / (16 * MT);
+  // warps that share a row block: few, so that what an item costs besides its
+  // boxes (about 0.7 boxes) comes seldom, but enough to keep every SM busy
+  double best = 0;
+  for (int ks = 1; ks <= kWarps; ks *= 2) {
+    const int64_t slices = (all + ks - 1) / ks, rb = kWarps / ks;
+    const int64_t rounds = ((rows + rb - 1) / rb + kPlanSms - 1) / kPlanSms;
+    const double cost = (double)rounds * ((double)slices + 0.7);
+    if (ks == 1 || cost < best) {
+      best = cost;
+      p->ks = ks;
+      p->slices = (int)slices;
+      p->rb = (int)rb;
+    }
+    if (ks >= all) break;
+  }
+  p->all = (int)all;
+  p->mask = 0x000f000fu;
+  p->magic = 0x43004300u;
+  p->items = (int)((rows + p->rb - 1) / p->rb);
+  p->xboxes = whole ? p->ks * p->slices : p->ks;
+  const int64_t left = kSmemMost - red - kWarps * kMostStages * 8 - (int64_t)p->xboxes * NT * 2 * kXChunk;
+  p->stages = left < 0 ? 0 : (int)(left / (kWarps * box));
+  if (p->stages > kMostStages) p->stages = kMostStages;
+  return p->stages >= 2;
+}
+
 template <int G, bool ZEROS, int MT, int NT>
-cudaError_t launch_nt(const W4Args& a, cudaStream_t s) {
-  constexpr int kBoxBytes = 16 * MT * 128, kRed = 16 * MT * 8 * NT;
-  constexpr int fixed = (NT == 1 ? 2 : 1) * kWarps * kRed * 4 + 2 * kMostStages * 8;
-  constexpr int xbox = NT * 2 * kXChunk;
-  constexpr int kHalf = 113 * 1024, kWhole = 226 * 1024;
-  W4Plan p;
-  const int64_t all = (a.K + kBox - 1) / kBox;
-  p.slices = (int)((all + kWarps - 1) / kWarps);
-  p.boxes = (int)((all + p.slices - 1) / p.slices);
-  p.rb = kWarps / p.boxes;
-  const int stage = p.boxes * p.rb * kBoxBytes;
-  // the token values of a whole row where three stages still fit beside them
-  p.xboxes = fixed + all * xbox + 3 * (int64_t)stage <= kWhole ? (int)all : p.boxes;
-  const int need = fixed + p.xboxes * xbox;
-  const int room = MT == 1 && need + 3 * stage <= kHalf ? kHalf : kWhole;
-  p.stages = (room - need) / stage;
-  if (p.stages > kMostStages) p.stages = kMostStages;
-  if (p.stages < 1) return cudaErrorInvalidValue;
-  const int smem = need + p.stages * stage;
-  p.items = ((a.N + 16 * MT - 1) / (16 * MT) + p.rb - 1) / p.rb;
+cudaError_t launch_plan(const W4Args& a, const W4Plan& p, cudaStream_t s) {
+  const int smem = kWarps * p.stages * 16 * MT * 128 + p.xboxes * NT * 2 * kXChunk +
+                   kWarps * 16 * MT * 8 * NT * 4 + kWarps * kMostStages * 8;
   CUtensorMap map;
   memset(&map, 0, sizeof(map));
   if (!encode_codes(&map, a, 16 * MT)) return cudaErrorInvalidValue;
@@ -456,20 +501,28 @@ cudaError_t launch_nt(const W4Args& a, cudaStream_t s) {
   e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int64_t most = (int64_t)sms * (room == kHalf ? 2 : 1);
-  const dim3 grid((unsigned)(p.items < most ? p.items : most),
+  const dim3 grid((unsigned)(p.items < sms ? p.items : sms),
                   (unsigned)((a.M + 8 * NT - 1) / (8 * NT)));
   kern<<<grid, kThreads, smem, s>>>(a, p, map);
   return cudaGetLastError();
 }
 
-// Tokens are taken 8 NT at a time.  From two token tiles on a warp takes 32
-// outputs, so that a token value read from shared memory serves two products.
+// A warp takes 32 outputs, so that a token value read from shared memory serves
+// two products; 16 where a ring of two such boxes does not fit beside the token
+// values of a whole row; and where neither fits, the token values are read
+// again for each slice.
+template <int G, bool ZEROS, int NT>
+cudaError_t launch_nt(const W4Args& a, cudaStream_t s) {
+  W4Plan p;
+  if (make_plan(a, 2, NT, true, &p)) return launch_plan<G, ZEROS, 2, NT>(a, p, s);
+  if (make_plan(a, 1, NT, true, &p)) return launch_plan<G, ZEROS, 1, NT>(a, p, s);
+  if (make_plan(a, 1, NT, false, &p)) return launch_plan<G, ZEROS, 1, NT>(a, p, s);
+  return cudaErrorInvalidValue;
+}
+
 template <int G, bool ZEROS>
 cudaError_t launch_z(const W4Args& a, cudaStream_t s) {
-  if (a.M <= 8) return launch_nt<G, ZEROS, 1, 1>(a, s);
-  if (a.M <= 16) return launch_nt<G, ZEROS, 2, 2>(a, s);
-  return launch_nt<G, ZEROS, 2, 4>(a, s);
+  return a.M <= 8 ? launch_nt<G, ZEROS, 1>(a, s) : launch_nt<G, ZEROS, 2>(a, s);
 }
 
 template <int G>

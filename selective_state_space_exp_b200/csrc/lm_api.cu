@@ -193,7 +193,7 @@ int check_w4(int64_t M, int64_t N, int64_t K, int32_t group) {
   if (M < 0 || N < 1 || K < 1 || group < 1) return M3_ERR_INVALID_ARGUMENT;
   if (group != 32 && group != 64 && group != 128) return M3_ERR_UNSUPPORTED;
   if (K % group != 0) return M3_ERR_INVALID_ARGUMENT;
-  const int64_t most = kMaxExtent - 256;
+  const int64_t most = kMaxExtent / 2;
   if (M >= most || N >= most || K >= most) return M3_ERR_UNSUPPORTED;
   if (N > kMaxElems / K || M > kMaxElems / K || M > kMaxElems / N) return M3_ERR_UNSUPPORTED;
   return M3_OK;
