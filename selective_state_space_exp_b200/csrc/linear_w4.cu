@@ -69,18 +69,23 @@ __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t m
   return r;
 }
 
-__device__ bool w4_wait(uint64_t* bar, uint32_t parity, int* status) {
+// Waits for a phase: the timer is read only every so many tries (each try may
+// itself suspend for a while).
+__device__ __forceinline__ bool w4_wait(uint64_t* bar, uint32_t parity, int* status) {
   if (mbar_try_wait(bar, parity)) return true;
-  unsigned long long t0, t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
-  while (!mbar_try_wait(bar, parity)) {
+  unsigned long long t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    unsigned long long t;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    if (t0 == 0) t0 = t;
     if (t - t0 > kWaitNs) {
       if (status) atomicCAS(status, 0, (int)M3_ERR_TIMEOUT);
       return false;
     }
   }
-  return true;
 }
 
 // Input of word w (0..3) of lane column c (0..3) in a chunk of 128: per group a
@@ -525,9 +530,549 @@ cudaError_t launch_z(const W4Args& a, cudaStream_t s) {
   return a.M <= 8 ? launch_nt<G, ZEROS, 1>(a, s) : launch_nt<G, ZEROS, 2>(a, s);
 }
 
+// ---- tcgen05 form ---------------------------------------------------------------
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[N]) {
+  static_assert(N == 8 || N == 16, "columns");
+  if constexpr (N == 16) {
+    tmem_ld16(taddr, v);
+  } else {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                   "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr));
+  }
+}
+
+// 16 consecutive 32-bit columns of this thread's TMEM lane (warp-wide).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15])
+      : "memory");
+}
+
+// D (TMEM) [+]= A (TMEM) * B (smem), issued by one thread.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int c0, int c1,
+                                        uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// A place in a ring of n slots and the parity of its current use.
+struct Turn {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++slot == n) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+constexpr int kTileRows = 128;               // outputs of a tile
+constexpr int kStep = 256;                   // inputs of a step
+constexpr int kCodeBox = kTileRows * 128;    // bytes: a step's codes
+constexpr int kABufs = 2, kACols = kStep / 2;  // TMEM: a step's weights, bf16 pairs
+constexpr int kDCols = 512 - kABufs * kACols;  // TMEM left for sums
+constexpr int kBlock = 8;                    // groups whose scales are staged at a time
+constexpr int kWG = 2;                       // warpgroups of each of the two roles below
+constexpr int kWorkers = 4 * kWG;            // warps that decode, and as many that add up
+constexpr int kTcThreads = 32 * (2 * kWorkers + 4);
+
+template <int G, int NTOK>
+struct TcCfg {
+  // Sums of SUB inputs each, CI of them accumulated in turn: MMAs into one
+  // accumulator wait on each other, so few tokens want several chains.
+  static constexpr int CI = NTOK >= 128 ? 1 : NTOK == 64 ? 2 : 4;
+  static constexpr int SUB = CI == 1 ? G : G < 64 ? G : 64;
+  static constexpr int SETS = kStep / SUB / CI;         // of a step
+  static constexpr int DBUFS = kDCols / (CI * NTOK);    // sets in TMEM
+  static constexpr int COLS = NTOK / kWG;               // tokens of an adding thread
+  static constexpr int XBYTES = NTOK * kStep * 2;       // a step's token values
+  static constexpr int XBUFS = NTOK >= 128 ? 2 : 4;
+  static constexpr int CBUFS = NTOK >= 128 ? 4 : NTOK == 64 ? 4 : 8;
+  static constexpr int X_OFF = CBUFS * kCodeBox;
+  static constexpr int P_OFF = X_OFF + XBUFS * XBYTES;  // scales, then zero points
+  static constexpr int PBYTES = kBlock * kTileRows * 4;
+  static constexpr int BAR_OFF = P_OFF + 4 * PBYTES;
+  static constexpr int BARS = 2 * CBUFS + 2 * XBUFS + kABufs + 2 * DBUFS + 4 + 1;
+  static constexpr int SMEM = BAR_OFF + BARS * 8 + 16;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(NTOK * kTileRows * 4 <= P_OFF, "the split sums reuse the rings");
+};
+
+struct TcPlan {
+  int tiles;     // of 128 outputs
+  int split;     // CTAs of a cluster that share a tile's inputs
+  int steps;     // of a row
+  int per;       // steps of one split, a multiple of what a block of scales covers
+  uint32_t mask, magic;
+};
+
+template <int G, bool ZEROS, int NTOK>
+__global__ void __launch_bounds__(kTcThreads, 1)
+w4_tc_kernel(const W4Args a, const TcPlan p, const __grid_constant__ CUtensorMap cmap,
+             const __grid_constant__ CUtensorMap xmap) {
+  using Cf = TcCfg<G, NTOK>;
+  constexpr int NG = kStep / G;             // groups of a step
+  constexpr int CB = kBlock / NG;           // steps of a block of scales
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((smem_u32(sm) & 1023u) != 0) {
+    if (threadIdx.x == 0 && a.status) atomicCAS(a.status, 0, (int)M3_ERR_CUDA);
+    return;
+  }
+  float* s_scale = reinterpret_cast<float*>(sm + Cf::P_OFF);                         // [2][8][128]
+  uint32_t* s_zero = reinterpret_cast<uint32_t*>(sm + Cf::P_OFF + 2 * Cf::PBYTES);  // [2][8][128]
+  uint64_t* c_full = reinterpret_cast<uint64_t*>(sm + Cf::BAR_OFF);
+  uint64_t* c_empty = c_full + Cf::CBUFS;
+  uint64_t* x_full = c_empty + Cf::CBUFS;
+  uint64_t* a_full = x_full + Cf::XBUFS;
+  uint64_t* s_done = a_full + kABufs;       // a step's MMAs: its weights and token values are free
+  uint64_t* d_full = s_done + Cf::XBUFS;
+  uint64_t* d_empty = d_full + Cf::DBUFS;
+  uint64_t* p_full = d_empty + Cf::DBUFS;   // blocks of scales
+  uint64_t* p_empty = p_full + 2;
+  uint64_t* s_fin = p_empty + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_fin + 1);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Cf::CBUFS; ++i) { mbar_init(&c_full[i], 1); mbar_init(&c_empty[i], kWorkers); }
+    for (int i = 0; i < Cf::XBUFS; ++i) { mbar_init(&x_full[i], 1); mbar_init(&s_done[i], 1); }
+    for (int i = 0; i < kABufs; ++i) mbar_init(&a_full[i], 32 * kWorkers);
+    for (int i = 0; i < Cf::DBUFS; ++i) { mbar_init(&d_full[i], 1); mbar_init(&d_empty[i], 32 * kWorkers); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&p_full[i], 64); mbar_init(&p_empty[i], ZEROS ? 2 * kWorkers : kWorkers); }
+    mbar_init(s_fin, 1);
+    fence_mbar_init();
+  }
+  if (warp == 2 * kWorkers + 1) {
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = *s_tmem;                        // A buffers, then the groups' sums
+  const uint32_t td = tm + kABufs * kACols;
+
+  const int m0 = (int)blockIdx.y * NTOK;
+  const int rank = (int)blockIdx.x % p.split;         // of the cluster: its part of the inputs
+  const int tile0 = (int)blockIdx.x / p.split, tstep = (int)gridDim.x / p.split;
+  const int c0 = rank * p.per;
+  const int c1 = c0 + p.per < p.steps ? c0 + p.per : p.steps;
+  const int nc = c1 - c0;                             // steps of this CTA, in every tile
+  bool ok = true;
+
+  float* red = reinterpret_cast<float*>(sm);          // [NTOK][128], over the idle rings
+  if (warp < kWorkers) {
+    // ---- decoders: codes to bf16 weights in TMEM ------------------------------------
+    const int q = warp & 3, wg = warp >> 2;
+    const int r = 32 * q + lane;
+    const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+    const uint32_t magic = p.magic;
+    constexpr int WORDS = 32 / kWG;                   // of a row's step, a thread's part
+    Turn code, at, done;                              // done: two steps behind
+    uint32_t it = 0, blk = 0;                                 // blocks of scales so far
+    for (int tile = tile0; tile < p.tiles && ok; tile += tstep) {
+      for (int c = 0; c < nc; ++c) {
+        if (ZEROS && c % CB == 0) ok = w4_wait(&p_full[blk & 1u], (blk >> 1) & 1u, a.status);
+        ok = ok && w4_wait(&c_full[code.slot], code.phase, a.status);
+        if (it >= kABufs) {
+          ok = ok && w4_wait(&s_done[done.slot], done.phase, a.status);
+          done.next(Cf::XBUFS);
+        }
+        ++it;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint8_t* row = sm + code.slot * kCodeBox + r * 128;
+        uint32_t w[WORDS];
+#pragma unroll
+        for (int i = 0; i < WORDS / 4; ++i) {
+          const int piece = wg * (WORDS / 4) + i;
+          const uint4 v = *reinterpret_cast<const uint4*>(row + ((piece ^ (r & 7)) << 4));
+          w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+        }
+        const uint32_t* zs = s_zero + ((blk & 1u) * kBlock + (c % CB) * NG) * kTileRows + r;
+        const uint32_t acol = tm + lane_base + at.slot * kACols + wg * (4 * WORDS);
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 4) {
+          const uint32_t z = ZEROS ? zs[((wg * WORDS + i) * 8 / G) * kTileRows] : 0x43084308u;
+          uint32_t f[16];  // four words' codes in order: the pairs of one byte's halves
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t odd = w[i + j] >> 4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              f[4 * j + e] = sub_bf16x2(
+                  and_or(__byte_perm(w[i + j], odd, 0x4400u + 0x1111u * e), p.mask, magic), z);
+          }
+          tmem_st16(acol + i * 4, f);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        bar_arrive(&a_full[at.slot]);
+        at.next(kABufs);
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(&c_empty[code.slot]);
+          if (ZEROS && (c % CB == CB - 1 || c + 1 == nc)) bar_arrive(&p_empty[blk & 1u]);
+        }
+        if (c % CB == CB - 1 || c + 1 == nc) ++blk;
+        code.next(Cf::CBUFS);
+      }
+    }
+  } else if (warp < 2 * kWorkers) {
+    // ---- adders: the groups' sums out of TMEM, times their scales -------------------
+    const int q = warp & 3, wg = (warp - kWorkers) >> 2;
+    const int r = 32 * q + lane;
+    const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+    Turn dt;
+    uint32_t blk = 0;
+    float acc[Cf::COLS];
+#pragma unroll
+    for (int i = 0; i < Cf::COLS; ++i) acc[i] = 0.f;
+    for (int tile = tile0; tile < p.tiles && ok; tile += tstep) {
+      for (int c = 0; c < nc; ++c) {
+        if (c % CB == 0) ok = w4_wait(&p_full[blk & 1u], (blk >> 1) & 1u, a.status);
+        const float* sc = s_scale + ((blk & 1u) * kBlock + (c % CB) * NG) * kTileRows + r;
+#pragma unroll
+        for (int g = 0; g < Cf::SETS; ++g) {
+          float sv[Cf::CI];
+#pragma unroll
+          for (int h = 0; h < Cf::CI; ++h) sv[h] = sc[((g * Cf::CI + h) * Cf::SUB / G) * kTileRows];
+          ok = __all_sync(0xffffffffu, ok && w4_wait(&d_full[dt.slot], dt.phase, a.status));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t dcol = td + lane_base + dt.slot * (Cf::CI * NTOK) + wg * Cf::COLS;
+          constexpr int LD = Cf::COLS == 16 ? 16 : 8;  // few registers beside 64 sums
+#pragma unroll
+          for (int i = 0; i < Cf::COLS; i += LD) {
+#pragma unroll
+            for (int h = 0; h < Cf::CI; h += 2) {
+              uint32_t v[2][LD];
+              tmem_ld<LD>(dcol + h * NTOK + i, v[0]);
+              if (h + 1 < Cf::CI) tmem_ld<LD>(dcol + (h + 1) * NTOK + i, v[1]);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < LD; ++j) acc[i + j] = fmaf(sv[h], __uint_as_float(v[0][j]), acc[i + j]);
+              if (h + 1 < Cf::CI) {
+#pragma unroll
+                for (int j = 0; j < LD; ++j)
+                  acc[i + j] = fmaf(sv[h + 1 < Cf::CI ? h + 1 : h], __uint_as_float(v[1][j]), acc[i + j]);
+              }
+            }
+          }
+          tc_fence_before();
+          bar_arrive(&d_empty[dt.slot]);
+          dt.next(Cf::DBUFS);
+        }
+        if (!ok) break;
+        if (c % CB == CB - 1 || c + 1 == nc) {
+          __syncwarp();
+          if (lane == 0) bar_arrive(&p_empty[blk & 1u]);
+          ++blk;
+        }
+      }
+      if (ok && p.split == 1) {
+        const int64_t n = (int64_t)tile * kTileRows + r;
+        if (n < a.N) {
+          const float b = a.bias ? __ldg(a.bias + n) : 0.f;
+          const int left = (int)(a.M - m0) - wg * Cf::COLS;  // tokens from here
+          const int64_t at = (int64_t)(m0 + wg * Cf::COLS) * a.N + n;
+          if (a.out_f32) {
+            float* o = static_cast<float*>(a.out) + at;
+#pragma unroll
+            for (int i = 0; i < Cf::COLS; ++i, o += a.N)
+              if (i < left) *o = acc[i] + b;
+          } else {
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + at;
+#pragma unroll
+            for (int i = 0; i < Cf::COLS; ++i, o += a.N)
+              if (i < left) *o = __float2bfloat16_rn(acc[i] + b);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < Cf::COLS; ++i) acc[i] = 0.f;
+      }
+    }
+    if (p.split > 1) {  // one tile: its last sum is in, so the rings are idle
+#pragma unroll
+      for (int i = 0; i < Cf::COLS; ++i) red[(wg * Cf::COLS + i) * kTileRows + r] = acc[i];
+    }
+  } else if (warp >= 2 * kWorkers + 2) {
+    // ---- stagers: scales and zero points, a block of groups at a time ----------------
+    const int i0 = threadIdx.x - 32 * (2 * kWorkers + 2);  // 0..63: rows i0 and i0 + 64 of a tile
+    const int kg = (int)(a.K / G);
+    uint32_t blk = 0;
+    for (int tile = tile0; tile < p.tiles && ok; tile += tstep) {
+      for (int c = 0; c < nc; c += CB, ++blk) {
+        const uint32_t slot = blk & 1u;
+        const int g0 = (c0 + c) * NG;  // first group
+        uint32_t sw[2][kBlock / 2] = {}, zw[2][2] = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t row = (int64_t)tile * kTileRows + i0 + 64 * h;
+          const int left = row < a.N ? kg - g0 : 0;
+          const uint16_t* sp = static_cast<const uint16_t*>(a.scales) + row * kg + g0;
+          const uint8_t* zp = a.zeros + row * kg + g0;
+          if (left >= kBlock && kg % kBlock == 0) {  // g0 is a multiple of a block
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(sp));
+            sw[h][0] = v.x; sw[h][1] = v.y; sw[h][2] = v.z; sw[h][3] = v.w;
+            if constexpr (ZEROS) {
+              const uint2 z = __ldg(reinterpret_cast<const uint2*>(zp));
+              zw[h][0] = z.x; zw[h][1] = z.y;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < kBlock; ++j) {
+              if (j >= left) continue;
+              sw[h][j / 2] |= (uint32_t)__ldg(sp + j) << (16 * (j & 1));
+              if constexpr (ZEROS) zw[h][j / 4] |= (uint32_t)__ldg(zp + j) << (8 * (j & 3));
+            }
+          }
+        }
+        ok = w4_wait(&p_empty[slot], ((blk >> 1) & 1u) ^ 1u, a.status);
+        if (!ok) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int j = 0; j < kBlock; ++j) {
+            const int at = (slot * kBlock + j) * kTileRows + i0 + 64 * h;
+            s_scale[at] = __uint_as_float((j & 1) ? sw[h][j / 2] & 0xffff0000u : sw[h][j / 2] << 16);
+            if constexpr (ZEROS)
+              s_zero[at] = 0x43004300u + ((zw[h][j / 4] >> (8 * (j & 3))) & 15u) * 0x00010001u;
+          }
+        }
+        bar_arrive(&p_full[slot]);
+      }
+    }
+  } else if (warp == 2 * kWorkers && lane == 0) {
+    // ---- TMA ------------------------------------------------------------------------
+    Turn code, xt;
+    uint32_t nx = 0, ncode = 0;
+    for (int tile = tile0; tile < p.tiles && ok; tile += tstep) {
+      for (int c = 0; c < nc && ok; ++c) {
+        ok = w4_wait(&c_empty[code.slot], code.phase ^ 1u, a.status);
+        if (!ok) break;
+        mbar_expect_tx(&c_full[code.slot], kCodeBox);
+        tma_box(sm + code.slot * kCodeBox, &cmap, (c0 + c) * (kStep / 2), tile * kTileRows,
+                &c_full[code.slot]);
+        code.next(Cf::CBUFS);
+        ++ncode;
+        ok = w4_wait(&s_done[xt.slot], xt.phase ^ 1u, a.status);
+        if (!ok) break;
+        mbar_expect_tx(&x_full[xt.slot], Cf::XBYTES);
+        uint8_t* xs = sm + Cf::X_OFF + xt.slot * Cf::XBYTES;
+#pragma unroll
+        for (int i = 0; i < kStep / 64; ++i)
+          tma_box(xs + i * NTOK * 128, &xmap, (c0 + c) * kStep + i * 64, m0, &x_full[xt.slot]);
+        xt.next(Cf::XBUFS);
+        ++nx;
+      }
+    }
+    // the last copies have landed (bounded) before the block can exit
+    for (uint32_t k = ncode > Cf::CBUFS ? ncode - Cf::CBUFS : 0; k < ncode; ++k)
+      w4_wait(&c_full[k % Cf::CBUFS], (k / Cf::CBUFS) & 1u, a.status);
+    for (uint32_t k = nx > Cf::XBUFS ? nx - Cf::XBUFS : 0; k < nx; ++k)
+      w4_wait(&x_full[k % Cf::XBUFS], (k / Cf::XBUFS) & 1u, a.status);
+  } else if (warp == 2 * kWorkers + 1) {
+    // ---- MMA issue: the sums of a set in turn, so that none waits on the last ---------
+    const uint32_t idesc = idesc_bf16(kTileRows, NTOK, 0, 0);
+    Turn at, xt, dt;
+    for (int tile = tile0; tile < p.tiles && ok; tile += tstep) {
+      for (int c = 0; c < nc && ok; ++c) {
+        // three lanes wait at once
+        uint64_t* bar = lane == 0 ? &x_full[xt.slot] : lane == 1 ? &a_full[at.slot] : &d_empty[dt.slot];
+        const uint32_t ph = lane == 0 ? xt.phase : lane == 1 ? at.phase : dt.phase ^ 1u;
+        if (lane < 3) ok = w4_wait(bar, ph, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint64_t xd = sw128_desc(smem_u32(sm) + Cf::X_OFF + xt.slot * Cf::XBYTES, 16, 1024);
+        const uint32_t acol = tm + at.slot * kACols;
+        if (lane == 0) {
+#pragma unroll
+          for (int g = 0; g < Cf::SETS; ++g) {
+            if (g > 0) ok = w4_wait(&d_empty[dt.slot], dt.phase ^ 1u, a.status);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < Cf::SUB / 16; ++k) {
+#pragma unroll
+              for (int h = 0; h < Cf::CI; ++h) {
+                const int ks = (g * Cf::CI + h) * (Cf::SUB / 16) + k;  // of the step's sixteen
+                mma_bf16_ts(td + (dt.slot * Cf::CI + h) * NTOK, acol + ks * 8,
+                            xd + (uint64_t)((ks / 4) * NTOK * 8 + (ks % 4) * 2), idesc, k > 0);
+              }
+            }
+            mma_commit(&d_full[dt.slot]);
+            dt.next(Cf::DBUFS);
+          }
+          if (ok) mma_commit(&s_done[xt.slot]);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        dt.slot = __shfl_sync(0xffffffffu, dt.slot, 0);
+        dt.phase = __shfl_sync(0xffffffffu, dt.phase, 0);
+        at.next(kABufs);
+        xt.next(Cf::XBUFS);
+      }
+    }
+  }
+
+  // every MMA issued has completed before TMEM is released (bounded)
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2 * kWorkers + 1) {
+    if (lane == 0) {
+      mma_commit(s_fin);
+      w4_wait(s_fin, 0, a.status);
+    }
+    __syncwarp();
+    tmem_dealloc(tm, 512);
+  }
+  if (p.split == 1) return;
+
+  // ---- split inputs: the cluster's sums, added in rank order -------------------------
+  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+  {
+    const int mine = NTOK / p.split;  // tokens this CTA adds, four outputs at a time
+    for (int i = threadIdx.x; i < mine * (kTileRows / 4); i += kTcThreads) {
+      const int t = rank * mine + i / (kTileRows / 4), r = i % (kTileRows / 4) * 4;
+      const int64_t m = m0 + t, n = (int64_t)tile0 * kTileRows + r;
+      if (m >= a.M || n >= a.N) continue;
+      const uint32_t local = smem_u32(red + t * kTileRows + r);
+      float f[8][4];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k >= p.split) break;
+        uint32_t remote;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(k));
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(f[k][0]), "=f"(f[k][1]), "=f"(f[k][2]), "=f"(f[k][3])
+                     : "r"(remote));
+      }
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = f[0][j];
+#pragma unroll
+        for (int k = 1; k < 8; ++k)
+          if (k < p.split) v[j] += f[k][j];
+        if (a.bias && n + j < a.N) v[j] += __ldg(a.bias + n + j);
+      }
+      if (!M3_IN(m * a.N + n, a.M * a.N, a.status)) continue;
+      if (n + 4 <= a.N && a.N % 4 == 0) {
+        if (a.out_f32)
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + m * a.N + n) =
+              make_float4(v[0], v[1], v[2], v[3]);
+        else
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + m * a.N + n) =
+              make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n + j < a.N) io_store(a.out, m * a.N + n + j, v[j], !a.out_f32);
+      }
+    }
+  }
+  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+
+bool encode_tokens(CUtensorMap* m, const W4Args& a, int rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.M};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.K * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.A), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int G, bool ZEROS, int NTOK>
+cudaError_t launch_tc(const W4Args& a, cudaStream_t s) {
+  using Cf = TcCfg<G, NTOK>;
+  TcPlan p;
+  p.tiles = (int)((a.N + kTileRows - 1) / kTileRows);
+  p.steps = (int)((a.K + kStep - 1) / kStep);
+  p.mask = 0x000f000fu;
+  p.magic = 0x43004300u;
+  // splits of the inputs, of whole blocks of scales each
+  constexpr int unit = kBlock * G / kStep;  // steps of a block: 1, 2 or 4
+  const int64_t token_tiles = (a.M + NTOK - 1) / NTOK;
+  p.split = 1;
+  while (p.split < 8 && (int64_t)p.tiles * token_tiles * p.split * 2 <= kPlanSms &&
+         p.steps > unit * p.split)
+    p.split *= 2;
+  p.per = (p.steps + p.split - 1) / p.split;
+  p.per = (p.per + unit - 1) / unit * unit;
+  CUtensorMap cmap, xmap;
+  memset(&cmap, 0, sizeof(cmap));
+  memset(&xmap, 0, sizeof(xmap));
+  if (!encode_codes(&cmap, a, kTileRows) || !encode_tokens(&xmap, a, NTOK))
+    return cudaErrorInvalidValue;
+  auto kern = w4_tc_kernel<G, ZEROS, NTOK>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM);
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 0;
+  e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  // with a split every cluster has one tile: its sums meet once, at the end
+  const int64_t ctas = p.split > 1 ? (int64_t)p.tiles * p.split : p.tiles < sms ? p.tiles : sms;
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)token_tiles);
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = Cf::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)p.split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, p, cmap, xmap);
+}
+
+// Up to 16 tokens the mma.sync form: the tcgen05 one pays the same for any few
+// tokens (50257 x 2048, groups of 128, one token: 27.0 us against 17.3 us; 16
+// tokens: 27.6 against 24.7; 32 tokens: 30 against 47).
+template <int G, bool ZEROS>
+cudaError_t launch_m(const W4Args& a, cudaStream_t s) {
+  if (a.M <= 16) return launch_z<G, ZEROS>(a, s);
+  if (a.M <= 32) return launch_tc<G, ZEROS, 32>(a, s);
+  if (a.M <= 64) return launch_tc<G, ZEROS, 64>(a, s);
+  return launch_tc<G, ZEROS, 128>(a, s);
+}
+
 template <int G>
 cudaError_t launch_g(const W4Args& a, cudaStream_t s) {
-  return a.zeros ? launch_z<G, true>(a, s) : launch_z<G, false>(a, s);
+  return a.zeros ? launch_m<G, true>(a, s) : launch_m<G, false>(a, s);
 }
 
 // One warp per group: round to nearest, scale and zero point of the group's
