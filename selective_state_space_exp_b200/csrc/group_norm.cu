@@ -15,24 +15,34 @@
 // of each output.  Two forms, chosen by what one (sample, group) slice is:
 //   unit kernels   one position per sample (every token its own sample): a
 //                  slice is C / G contiguous values, held in the registers of
-//                  up to 32 lanes, so statistics and result take one read.
+//                  some lanes (or warps), so statistics and result take one read.
 //                  A thread keeps its channels over all the rows it visits, so
 //                  w, b and the sums for dw, db stay in registers.
-//   slice kernels  everything else: partial statistics over splits of a
-//                  slice's positions, then a second pass that applies them
-//                  (its reads come from L2 where the tensor fits there).
+//   slice kernels  everything else: partial sums over splits of a sample's
+//                  positions, joined by a small kernel, then a second pass that
+//                  applies them (its reads come from L2 where the tensors fit
+//                  there).  Blocks cover whole rows, so that what runs at one
+//                  time reads neighbouring memory.  (Slices held in the shared
+//                  memory of clusters, read once, measured slower: 56 against
+//                  54 us forward and 169 against 100 us backward at 8 x 2048 x
+//                  2048, for the clusters leave SMs idle between them.)
 // Statistics are fp32: in the unit kernels the mean first, then the deviations
-// from it (whose own mean corrects it) and their squares; in the slice kernels
-// per-vector means and deviations merged pairwise (Chan, Golub and LeVeque), so
-// a large common offset is not squared.  No atomics: dw and db are partial sums in the workspace, added in
-// a fixed order.
+// from it (whose own mean corrects it) and their squares; in the others sums about
+// one of the values, merged pairwise as counts, means and squared deviations (Chan,
+// Golub and LeVeque): a large common offset is not squared.  No atomics: dw and db are partial sums in the workspace, added
+// in a fixed order.
+#include <type_traits>
+
 #include "lm_ops.cuh"
+#include "tc_ptx.cuh"
 
 namespace m3 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxLaneElems = 32;  // values one lane of a unit kernel may hold
+// Values one lane of a unit kernel may hold: its weights, biases and their sums
+// are as many registers each.
+constexpr int kMaxLaneElems = 16;
 
 template <int BYTES> struct Raw;
 template <> struct Raw<2> { using T = uint16_t; };
@@ -40,62 +50,126 @@ template <> struct Raw<4> { using T = uint32_t; };
 template <> struct Raw<8> { using T = uint2; };
 template <> struct Raw<16> { using T = uint4; };
 
-// V elements of the io type as one aligned access.
+// V elements of the io type as one aligned access, held as pairs of fp32 (one
+// packed instruction does a pair's arithmetic); with V = 1 the pair's second
+// half is 0 and not stored.
 template <bool BF16, int V>
 struct Io {
   static constexpr int ES = BF16 ? 2 : 4;
+  static constexpr int P = (V + 1) / 2;  // pairs
   using R = typename Raw<V * ES>::T;
   __device__ static R load(const void* p, int64_t i) {
     return *reinterpret_cast<const R*>(static_cast<const char*>(p) + i * ES);
   }
-  __device__ static void unpack(const R& r, float (&f)[V]) {
-    if constexpr (BF16) {
-      const __nv_bfloat16* h = reinterpret_cast<const __nv_bfloat16*>(&r);
+  __device__ static void unpack(const R& r, float2 (&f)[P]) {
+    if constexpr (V == 1) {
+      f[0].x = BF16 ? __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(&r) << 16)
+                    : *reinterpret_cast<const float*>(&r);
+      f[0].y = 0.f;
+    } else if constexpr (BF16) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
 #pragma unroll
-      for (int e = 0; e < V; ++e) f[e] = __bfloat162float(h[e]);
+      for (int e = 0; e < P; ++e)
+        f[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
     } else {
       const float* h = reinterpret_cast<const float*>(&r);
 #pragma unroll
-      for (int e = 0; e < V; ++e) f[e] = h[e];
+      for (int e = 0; e < P; ++e) f[e] = make_float2(h[2 * e], h[2 * e + 1]);
     }
   }
-  __device__ static void store(void* p, int64_t i, const float (&f)[V]) {
+  __device__ static void store(void* p, int64_t i, const float2 (&f)[P]) {
     R r;
-    if constexpr (BF16) {
-      __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(&r);
+    if constexpr (V == 1) {
+      if constexpr (BF16)
+        *reinterpret_cast<__nv_bfloat16*>(&r) = __float2bfloat16_rn(f[0].x);
+      else
+        *reinterpret_cast<float*>(&r) = f[0].x;
+    } else if constexpr (BF16) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(&r);
 #pragma unroll
-      for (int e = 0; e < V; ++e) h[e] = __float2bfloat16_rn(f[e]);
+      for (int e = 0; e < P; ++e) w[e] = tc::pack_bf16(f[e].x, f[e].y);
     } else {
       float* h = reinterpret_cast<float*>(&r);
 #pragma unroll
-      for (int e = 0; e < V; ++e) h[e] = f[e];
+      for (int e = 0; e < P; ++e) {
+        h[2 * e] = f[e].x;
+        h[2 * e + 1] = f[e].y;
+      }
     }
     *reinterpret_cast<R*>(static_cast<char*>(p) + i * ES) = r;
   }
 };
 
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+using tc::ffma2;
+using tc::fmul2;
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// 1 / (1 + e^-v) with the quotient's edge cases: __fdividef gives 0 for a
-// divisor beyond 2^126, which is sigma's limit there.
-__device__ __forceinline__ float activate(int act, float u, float z) {
-  if (act == M3_ACT_SILU) return u * sigmoid(u);
-  if (act == M3_ACT_GATE) return u * z * sigmoid(z);
+// 1 / (1 + e^-v) of a pair; beyond the exponential's range the quotient is 0,
+// sigma's limit.
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+  const float2 t = fmul2(v, both(-1.4426950408889634f));
+  const float2 d = fadd2(make_float2(tc::ex2(t.x), tc::ex2(t.y)), both(1.f));
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+  return r;
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 activate(float2 u, float2 z) {
+  if constexpr (ACT == M3_ACT_SILU) return fmul2(u, sigmoid2(u));
+  if constexpr (ACT == M3_ACT_GATE) return fmul2(u, fmul2(z, sigmoid2(z)));
   return u;
 }
 
 // g = dL/du, and dz for the gate
-__device__ __forceinline__ float act_grad(int act, float u, float z, float dy, float& dz) {
-  if (act == M3_ACT_SILU) {
-    const float s = sigmoid(u);
-    return dy * s * fmaf(u, 1.f - s, 1.f);
+template <int ACT>
+__device__ __forceinline__ float2 act_grad(float2 u, float2 z, float2 dy, float2& dz) {
+  if constexpr (ACT == M3_ACT_SILU) {
+    const float2 s = sigmoid2(u);
+    return fmul2(fmul2(dy, s), ffma2(u, ffma2(s, both(-1.f), both(1.f)), both(1.f)));
   }
-  if (act == M3_ACT_GATE) {
-    const float s = sigmoid(z);
-    dz = dy * u * s * fmaf(z, 1.f - s, 1.f);
-    return dy * z * s;
+  if constexpr (ACT == M3_ACT_GATE) {
+    const float2 s = sigmoid2(z), ds = fmul2(dy, s);
+    dz = fmul2(fmul2(ds, u), ffma2(z, ffma2(s, both(-1.f), both(1.f)), both(1.f)));
+    return fmul2(ds, z);
   }
   return dy;
+}
+
+// A group's weights and biases from channel c on (1 and 0 where there are none;
+// 0 and 0 in the unused half of V = 1, which keeps it out of every sum).
+template <int V>
+__device__ __forceinline__ void load_params(const NormArgs& a, int64_t c, bool in,
+                                            float2 (&w)[(V + 1) / 2], float2 (&b)[(V + 1) / 2]) {
+  float fw[V + 1], fb[V + 1];
+  fw[V] = fb[V] = 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    fw[e] = in && a.w ? __ldg(a.w + c + e) : 1.f;
+    fb[e] = in && a.b ? __ldg(a.b + c + e) : 0.f;
+  }
+#pragma unroll
+  for (int e = 0; e < (V + 1) / 2; ++e) {
+    w[e] = make_float2(fw[2 * e], fw[2 * e + 1]);
+    b[e] = make_float2(fb[2 * e], fb[2 * e + 1]);
+  }
+}
+
+// x - m of a pair; the unused half of V = 1 stays 0.
+template <int V>
+__device__ __forceinline__ float2 minus(float2 x, float m) {
+  const float2 d = fadd2(x, make_float2(-m, -m));
+  return V == 1 ? make_float2(d.x, 0.f) : d;
 }
 
 // ---- unit kernels: one position per sample -----------------------------------
@@ -111,180 +185,246 @@ __device__ __forceinline__ float lane_sum(float v, int L) {
   return v;
 }
 
-template <bool BF16, int V, int NV>
+// Sums of two values over a unit's lanes.  LANES: their number where it is known
+// at compile time, 0 where it is at most 32, -1 where a unit is several warps
+// (which add up in shared memory; every thread of the block takes part).
+template <int LANES>
+__device__ __forceinline__ float2 unit_sum(float2 v, int L, float2* s_red) {
+  if constexpr (LANES > 0) {
+#pragma unroll
+    for (int o = LANES >> 1; o > 0; o >>= 1)
+      v = fadd2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o),
+                               __shfl_xor_sync(0xffffffffu, v.y, o)));
+  } else if constexpr (LANES == 0) {
+    v = make_float2(lane_sum(v.x, L), lane_sum(v.y, L));
+  } else {
+    v = make_float2(lane_sum(v.x, 32), lane_sum(v.y, 32));
+    const int warp = threadIdx.x >> 5, per = L >> 5, first = warp / per * per;
+    if ((threadIdx.x & 31) == 0) s_red[warp] = v;
+    __syncthreads();
+    v = s_red[first];
+    for (int i = 1; i < per; ++i) v = fadd2(v, s_red[first + i]);
+    __syncthreads();
+  }
+  return v;
+}
+
+// What a thread of the unit kernels walks over: its vectors of the rows ry, ry +
+// step, ... of a column of units.
+struct Walk {
+  int lane, unit, ry, rows;  // rows: how many it has
+  int64_t first, step;       // elements: its first vector of its first row, and a row on
+  int64_t stat, sstep;       // the same in [samples][groups]
+  int64_t col;               // first channel of its first vector
+  bool any;                  // whether it has a unit
+};
+__device__ __forceinline__ Walk walk_of(const NormArgs& a, const UnitPlan& p, int L, int V) {
+  Walk o;
+  o.lane = threadIdx.x % L;
+  const int slot = threadIdx.x / L;
+  o.unit = slot % p.ub;
+  o.ry = slot / p.ub;
+  const int64_t g = (int64_t)blockIdx.x * p.ub + o.unit;
+  const int64_t row = (int64_t)blockIdx.y * p.ty + o.ry, step = (int64_t)gridDim.y * p.ty;
+  o.any = o.ry < p.ty && g < a.groups;
+  o.rows = o.any && row < a.batch ? (int)((a.batch - row + step - 1) / step) : 0;
+  o.col = g * a.cg + o.lane * V;
+  o.first = row * a.channels + o.col;
+  o.step = step * a.channels;
+  o.stat = row * a.groups + g;
+  o.sstep = step * a.groups;
+  return o;
+}
+// Rows that any thread of the block has: all take part in a unit's sums.
+__device__ __forceinline__ int most_rows(const NormArgs& a, const UnitPlan& p) {
+  const int64_t row = (int64_t)blockIdx.y * p.ty, step = (int64_t)gridDim.y * p.ty;
+  return row < a.batch ? (int)((a.batch - row + step - 1) / step) : 0;
+}
+
+template <bool BF16, int V, int NV, int LANES, int ACT>
 __global__ void __launch_bounds__(kThreads) unit_fwd_kernel(const NormArgs a, const UnitPlan p) {
   using X = Io<BF16, V>;
-  const int lane = threadIdx.x % p.L, slot = threadIdx.x / p.L;
-  const int unit = slot % p.ub, ry = slot / p.ub;
-  const int64_t g = (int64_t)blockIdx.x * p.ub + unit;
-  const bool mine = ry < p.ty && g < a.groups;
+  using R = typename X::R;
+  constexpr int P = X::P;
+  __shared__ float2 s_red[kThreads / 32];
+  const int L = LANES > 0 ? LANES : p.L;
+  const Walk o = walk_of(a, p, L, V);
   const int nvec = (int)(a.cg / V);
-  float w[NV][V], b[NV][V];
+  const int gap = L * V * X::ES;  // bytes between a lane's vectors
+  float2 w[NV][P], b[NV][P];
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int v = k * p.L + lane;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const bool in = mine && v < nvec;
-      const int64_t c = g * a.cg + (int64_t)v * V + e;
-      w[k][e] = in && a.w ? __ldg(a.w + c) : 1.f;
-      b[k][e] = in && a.b ? __ldg(a.b + c) : 0.f;
-    }
-  }
+  for (int k = 0; k < NV; ++k)
+    load_params<V>(a, o.col + (int64_t)k * L * V, o.any && k * L + o.lane < nvec, w[k], b[k]);
   const float inv_n = 1.f / (float)a.cg;
-  for (int64_t r0 = (int64_t)blockIdx.y * p.ty; r0 < a.batch; r0 += (int64_t)gridDim.y * p.ty) {
-    const int64_t row = r0 + ry;
-    const bool on = mine && row < a.batch;
-    const int64_t base = row * a.channels + g * a.cg;
-    float x[NV][V], z[NV][V];
-    typename X::R xr[NV], zr[NV];
+  const char* px = static_cast<const char*>(a.x) + o.first * X::ES;
+  const char* pz = static_cast<const char*>(a.z) + o.first * X::ES;
+  char* py = static_cast<char*>(a.y) + o.first * X::ES;
+  const int64_t step = o.step * X::ES;
+  int64_t stat = o.stat;
+  R xn[NV], zn[NV];  // the next row, on its way while this one is worked on
+  auto fetch = [&] {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int v = k * p.L + lane;
-      if (on && v < nvec) {
-        xr[k] = X::load(a.x, base + (int64_t)v * V);
-        if (a.act == M3_ACT_GATE) zr[k] = X::load(a.z, base + (int64_t)v * V);
-      }
+      if (k * L + o.lane >= nvec) break;
+      xn[k] = *reinterpret_cast<const R*>(px + k * gap);
+      if constexpr (ACT == M3_ACT_GATE) zn[k] = *reinterpret_cast<const R*>(pz + k * gap);
     }
-    float sum = 0.f;
+    px += step;
+    pz += step;
+  };
+  if (o.rows > 0) fetch();
+  const int most = most_rows(a, p);
+  for (int r = 0; r < most; ++r) {
+    float2 x[NV][P];
+    R z0[NV];
+    float2 sum = both(0.f);
+    const bool on = r < o.rows;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if (on && k * p.L + lane < nvec) {
-        X::unpack(xr[k], x[k]);
+      if (!on || k * L + o.lane >= nvec) break;
+      X::unpack(xn[k], x[k]);
+      if constexpr (ACT == M3_ACT_GATE) z0[k] = zn[k];
 #pragma unroll
-        for (int e = 0; e < V; ++e) sum += x[k][e];
-      }
+      for (int e = 0; e < P; ++e) sum = fadd2(sum, x[k][e]);
     }
+    if (r + 1 < o.rows) fetch();
     // deviations from the rounded mean; their own mean `off` corrects it
-    const float mean0 = lane_sum(sum, p.L) * inv_n;
-    float sq = 0.f, dev = 0.f;
+    const float mean0 = unit_sum<LANES>(make_float2(sum.x + sum.y, 0.f), L, s_red).x * inv_n;
+    float2 sq = both(0.f), dev = both(0.f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if (on && k * p.L + lane < nvec) {
+      if (!on || k * L + o.lane >= nvec) break;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          x[k][e] -= mean0;
-          dev += x[k][e];
-          sq = fmaf(x[k][e], x[k][e], sq);
-        }
+      for (int e = 0; e < P; ++e) {
+        x[k][e] = minus<V>(x[k][e], mean0);
+        dev = fadd2(dev, x[k][e]);
+        sq = ffma2(x[k][e], x[k][e], sq);
       }
     }
-    const float off = lane_sum(dev, p.L) * inv_n;
-    const float var = fmaf(-off, off, lane_sum(sq, p.L) * inv_n);
-    const float mean = mean0 + off, rstd = 1.f / sqrtf(var + a.eps);
-    if (!on) continue;
-    if (lane == 0 && M3_IN(row * a.groups + g, a.batch * a.groups, a.status)) {
-      if (a.mean) a.mean[row * a.groups + g] = mean;
-      if (a.rstd) a.rstd[row * a.groups + g] = rstd;
-    }
+    const float2 t = unit_sum<LANES>(make_float2(dev.x + dev.y, sq.x + sq.y), L, s_red);
+    if (on) {
+      const float off = t.x * inv_n;
+      const float rstd = rsqrtf(fmaf(-off, off, t.y * inv_n) + a.eps);
+      if (o.lane == 0 && M3_IN(stat, a.batch * a.groups, a.status)) {
+        if (a.mean) a.mean[stat] = mean0 + off;
+        if (a.rstd) a.rstd[stat] = rstd;
+      }
+      const float2 scale = both(rstd), shift = both(-off * rstd);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = k * p.L + lane;
-      if (v >= nvec) continue;
-      if (a.act == M3_ACT_GATE) X::unpack(zr[k], z[k]);
-      float o[V];
+      for (int k = 0; k < NV; ++k) {
+        if (k * L + o.lane >= nvec) break;
+        float2 z[P], y[P];
+        if constexpr (ACT == M3_ACT_GATE) X::unpack(z0[k], z);
 #pragma unroll
-      for (int e = 0; e < V; ++e)
-        o[e] = activate(a.act, fmaf((x[k][e] - off) * rstd, w[k][e], b[k][e]), z[k][e]);
-      if (M3_IN(base + (int64_t)v * V + V - 1, a.batch * a.channels, a.status))
-        X::store(a.y, base + (int64_t)v * V, o);
+        for (int e = 0; e < P; ++e)
+          y[e] = activate<ACT>(ffma2(ffma2(x[k][e], scale, shift), w[k][e], b[k][e]), z[e]);
+        if (M3_IN((py - static_cast<char*>(a.y)) + k * gap, a.batch * a.channels * X::ES, a.status))
+          X::store(py + k * gap, 0, y);
+      }
     }
+    py += step;
+    stat += o.sstep;
   }
 }
 
-template <bool BF16, int V, int NV>
+constexpr int kUnitRows = 2;  // rows whose loads are in flight together
+
+template <bool BF16, int V, int NV, int LANES, int ACT>
 __global__ void __launch_bounds__(kThreads) unit_bwd_kernel(const NormArgs a, const UnitPlan p) {
   using X = Io<BF16, V>;
-  const int lane = threadIdx.x % p.L, slot = threadIdx.x / p.L;
-  const int unit = slot % p.ub, ry = slot / p.ub;
-  const int64_t g = (int64_t)blockIdx.x * p.ub + unit;
-  const bool mine = ry < p.ty && g < a.groups;
+  constexpr int P = X::P;
+  __shared__ float2 s_red[kThreads / 32];
+  const int L = LANES > 0 ? LANES : p.L;
+  const Walk o = walk_of(a, p, L, V);
   const int nvec = (int)(a.cg / V);
-  float w[NV][V], b[NV][V], dw[NV][V], db[NV][V];
+  const int gap = L * V * X::ES;  // bytes between a lane's vectors
+  float2 w[NV][P], b[NV][P], dw[NV][P], db[NV][P];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int v = k * p.L + lane;
+    load_params<V>(a, o.col + (int64_t)k * L * V, o.any && k * L + o.lane < nvec, w[k], b[k]);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const bool in = mine && v < nvec;
-      const int64_t c = g * a.cg + (int64_t)v * V + e;
-      w[k][e] = in && a.w ? __ldg(a.w + c) : 1.f;
-      b[k][e] = in && a.b ? __ldg(a.b + c) : 0.f;
-      dw[k][e] = db[k][e] = 0.f;
-    }
+    for (int e = 0; e < P; ++e) dw[k][e] = db[k][e] = both(0.f);
   }
   const float inv_n = 1.f / (float)a.cg;
-  for (int64_t r0 = (int64_t)blockIdx.y * p.ty; r0 < a.batch; r0 += (int64_t)gridDim.y * p.ty) {
-    const int64_t row = r0 + ry;
-    const bool on = mine && row < a.batch;
-    const int64_t base = row * a.channels + g * a.cg;
-    typename X::R xr[NV], yr[NV], zr[NV];
-    float mean = 0.f, rstd = 0.f;
-    if (on) {
-      mean = __ldg(a.mean + row * a.groups + g);
-      rstd = __ldg(a.rstd + row * a.groups + g);
-    }
+  const int64_t step = o.step * X::ES;
+  int64_t at = o.first * X::ES, stat = o.stat;
+  const char *px = static_cast<const char*>(a.x), *pd = static_cast<const char*>(a.dy),
+             *pz = static_cast<const char*>(a.z);
+  char *dx = static_cast<char*>(a.dx), *dz = static_cast<char*>(a.dz);
+  const int most = most_rows(a, p);
+  for (int r = 0; r < most; r += kUnitRows) {
+    typename X::R xr[kUnitRows][NV], yr[kUnitRows][NV], zr[kUnitRows][NV];
+    float mean[kUnitRows], rstd[kUnitRows];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = k * p.L + lane;
-      if (on && v < nvec) {
-        xr[k] = X::load(a.x, base + (int64_t)v * V);
-        yr[k] = X::load(a.dy, base + (int64_t)v * V);
-        if (a.act == M3_ACT_GATE) zr[k] = X::load(a.z, base + (int64_t)v * V);
+    for (int u = 0; u < kUnitRows; ++u) {
+      if (r + u >= o.rows) break;
+      mean[u] = __ldg(a.mean + stat + u * o.sstep);
+      rstd[u] = __ldg(a.rstd + stat + u * o.sstep);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if (k * L + o.lane >= nvec) break;
+        const int64_t i = at + u * step + k * gap;
+        xr[u][k] = *reinterpret_cast<const typename X::R*>(px + i);
+        yr[u][k] = *reinterpret_cast<const typename X::R*>(pd + i);
+        if constexpr (ACT == M3_ACT_GATE) zr[u][k] = *reinterpret_cast<const typename X::R*>(pz + i);
       }
     }
-    float xh[NV][V], gw[NV][V], c1 = 0.f, c2 = 0.f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = k * p.L + lane;
-      if (!(on && v < nvec)) continue;
-      float dy[V], z[V], dz[V];
-      X::unpack(xr[k], xh[k]);
-      X::unpack(yr[k], dy);
-      if (a.act == M3_ACT_GATE) X::unpack(zr[k], z);
+    for (int u = 0; u < kUnitRows; ++u) {
+      const bool on = r + u < o.rows;
+      float2 xh[NV][P], gw[NV][P], c1 = both(0.f), c2 = both(0.f);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        xh[k][e] = (xh[k][e] - mean) * rstd;
-        const float u = fmaf(xh[k][e], w[k][e], b[k][e]);
-        const float gr = act_grad(a.act, u, z[e], dy[e], dz[e]);
-        dw[k][e] = fmaf(gr, xh[k][e], dw[k][e]);
-        db[k][e] += gr;
-        gw[k][e] = gr * w[k][e];
-        c1 += gw[k][e];
-        c2 = fmaf(gw[k][e], xh[k][e], c2);
+      for (int k = 0; k < NV; ++k) {
+        if (!on || k * L + o.lane >= nvec) break;
+        float2 dy[P], z[P], d[P];
+        X::unpack(xr[u][k], xh[k]);
+        X::unpack(yr[u][k], dy);
+        if constexpr (ACT == M3_ACT_GATE) X::unpack(zr[u][k], z);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          xh[k][e] = fmul2(minus<V>(xh[k][e], mean[u]), both(rstd[u]));
+          const float2 gr = act_grad<ACT>(ffma2(xh[k][e], w[k][e], b[k][e]), z[e], dy[e], d[e]);
+          dw[k][e] = ffma2(gr, xh[k][e], dw[k][e]);
+          db[k][e] = fadd2(db[k][e], gr);
+          gw[k][e] = fmul2(gr, w[k][e]);
+          c1 = fadd2(c1, gw[k][e]);
+          c2 = ffma2(gw[k][e], xh[k][e], c2);
+        }
+        if (ACT == M3_ACT_GATE && dz &&
+            M3_IN(at + u * step + k * gap, a.batch * a.channels * X::ES, a.status))
+          X::store(dz + at + u * step + k * gap, 0, d);
       }
-      if (a.act == M3_ACT_GATE && a.dz &&
-          M3_IN(base + (int64_t)v * V + V - 1, a.batch * a.channels, a.status))
-        X::store(a.dz, base + (int64_t)v * V, dz);
-    }
-    c1 = lane_sum(c1, p.L) * inv_n;
-    c2 = lane_sum(c2, p.L) * inv_n;
-    if (!on || !a.dx) continue;
+      const float2 c = unit_sum<LANES>(make_float2(c1.x + c1.y, c2.x + c2.y), L, s_red);
+      if (on && dx) {
+        const float2 s = both(rstd[u]), k1 = both(-c.x * inv_n * rstd[u]), k2 = both(-c.y * inv_n * rstd[u]);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = k * p.L + lane;
-      if (v >= nvec) continue;
-      float o[V];
+        for (int k = 0; k < NV; ++k) {
+          if (k * L + o.lane >= nvec) break;
+          float2 d[P];
 #pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = rstd * (gw[k][e] - c1 - xh[k][e] * c2);
-      if (M3_IN(base + (int64_t)v * V + V - 1, a.batch * a.channels, a.status))
-        X::store(a.dx, base + (int64_t)v * V, o);
+          for (int e = 0; e < P; ++e) d[e] = ffma2(gw[k][e], s, ffma2(xh[k][e], k2, k1));
+          if (M3_IN(at + u * step + k * gap, a.batch * a.channels * X::ES, a.status))
+            X::store(dx + at + u * step + k * gap, 0, d);
+        }
+      }
     }
+    at += kUnitRows * step;
+    stat += kUnitRows * o.sstep;
   }
   if (!a.ws) return;
   // the block's sums over its rows: row slots are added in shared memory
   extern __shared__ float s_sum[];  // [ty][ub * cg] twice
   const int width = p.ub * (int)a.cg;
-  if (ry < p.ty) {
+  if (o.ry < p.ty) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int v = k * p.L + lane;
-      if (v >= nvec) continue;
+      const int v = k * L + o.lane;
+      if (v >= nvec) break;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const int at = ry * width + unit * (int)a.cg + v * V + e;
-        s_sum[at] = dw[k][e];
-        s_sum[p.ty * width + at] = db[k][e];
+        const int i = o.ry * width + o.unit * (int)a.cg + v * V + e;
+        s_sum[i] = (e & 1) ? dw[k][e / 2].y : dw[k][e / 2].x;
+        s_sum[p.ty * width + i] = (e & 1) ? db[k][e / 2].y : db[k][e / 2].x;
       }
     }
   }
@@ -303,14 +443,6 @@ __global__ void __launch_bounds__(kThreads) unit_bwd_kernel(const NormArgs a, co
   }
 }
 
-// ---- slice kernels: any number of positions per sample -----------------------
-// blockIdx.x = sample * groups + group, blockIdx.y = split of the positions.
-// tx threads along the channels (vectors), ty along the positions.
-
-struct SlicePlan {
-  int V, tx, ty, splits;
-};
-
 // Positions of sample i in the token dimension (the checks of chain_of).
 __device__ __forceinline__ Chain rows_of(const NormArgs& a, int64_t i) {
   if (!a.cu_seqlens) return Chain{i * a.seqlen, a.seqlen};
@@ -327,7 +459,7 @@ struct Moments {
 __device__ __forceinline__ Moments merge(const Moments& p, const Moments& q) {
   const float n = p.n + q.n;
   if (n == 0.f) return Moments{0.f, 0.f, 0.f};
-  const float d = q.mean - p.mean, f = q.n / n;
+  const float d = q.mean - p.mean, f = __fdividef(q.n, n);
   return Moments{n, fmaf(d, f, p.mean), p.m2 + q.m2 + d * d * p.n * f};
 }
 __device__ __forceinline__ Moments shfl_merge(const Moments& m) {
@@ -342,252 +474,337 @@ __device__ __forceinline__ Moments shfl_merge(const Moments& m) {
   return r;
 }
 
+// ---- two passes over whole rows -------------------------------------------------
+// A block takes some positions of one sample (blockIdx.y = split) and a tile of
+// channels: as many whole groups as fit its threads, or a piece of one group
+// (blockIdx.x = sample and tile).  tx threads along the channels, one vector
+// each, ty along the positions: neighbouring threads read neighbouring memory.
+
+struct SlicePlan {
+  int V, tx, ty;
+  int gpt;     // groups of a tile
+  int pieces;  // tiles of a group, where one does not fit a block
+  int tiles;   // of a row
+  int splits;
+};
+
+// Rows whose loads are in flight together; fewer in the backward, where three
+// blocks an SM do better than two (both passes 79 us against 85 at 8 x 2048 x 2048).
+constexpr int kRowsAhead = 4, kBwdRowsAhead = 2;
+
 __device__ __forceinline__ void split_rows(const Chain& c, int splits, int64_t& r0, int64_t& r1) {
-  const int64_t per = (c.len + splits - 1) / splits;
+  const int64_t per = ((uint32_t)c.len + (uint32_t)splits - 1) / (uint32_t)splits;
   r0 = per * blockIdx.y < c.len ? per * blockIdx.y : c.len;
   r1 = r0 + per < c.len ? r0 + per : c.len;
 }
 
-template <bool BF16, int V>
-__global__ void __launch_bounds__(kThreads) slice_stats_kernel(const NormArgs a, const SlicePlan p) {
-  using X = Io<BF16, V>;
-  const int64_t sample = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
-  const Chain ch = rows_of(a, sample);
-  int64_t r0, r1;
-  split_rows(ch, p.splits, r0, r1);
-  const int tx = threadIdx.x % p.tx, ty = threadIdx.x / p.tx;
-  const int64_t nvec = a.cg / V;
-  Moments m{0.f, 0.f, 0.f};
-  if (ty < p.ty) {
-    for (int64_t v = tx; v < nvec; v += p.tx) {
-      for (int64_t r = r0 + ty; r < r1; r += p.ty) {
-        const typename X::R raw = X::load(a.x, (ch.base + r) * a.channels + g * a.cg + v * V);
-        float f[V];
-        X::unpack(raw, f);
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) s += f[e];
-        Moments q{(float)V, s * (1.f / V), 0.f};
-#pragma unroll
-        for (int e = 0; e < V; ++e) q.m2 = fmaf(f[e] - q.mean, f[e] - q.mean, q.m2);
-        m = merge(m, q);
-      }
-    }
+// Where a thread stands.
+struct Place {
+  int64_t sample, base, r0, r1, col;  // first row of the sample; its split; its vector's first channel
+  int tile, group, piece, tx, ty;     // group: of the tile (gpt: none)
+  bool on;
+};
+__device__ __forceinline__ Place place_of(const NormArgs& a, const SlicePlan& p) {
+  Place o;
+  o.sample = blockIdx.x / (unsigned)p.tiles;
+  o.tile = (int)(blockIdx.x % (unsigned)p.tiles);
+  const Chain ch = rows_of(a, o.sample);
+  o.base = ch.base;
+  split_rows(ch, p.splits, o.r0, o.r1);
+  o.tx = threadIdx.x % p.tx;
+  o.ty = threadIdx.x / p.tx;
+  const int nvec = (int)(a.cg / p.V);
+  if (p.pieces > 1) {
+    o.group = 0;
+    o.piece = o.tile % p.pieces;
+    const int v = o.piece * p.tx + o.tx;
+    o.col = (int64_t)(o.tile / p.pieces) * a.cg + (int64_t)v * p.V;
+    o.on = o.ty < p.ty && v < nvec;
+  } else {
+    o.group = o.tx / nvec;
+    o.piece = 0;
+    o.col = (int64_t)o.tile * p.gpt * a.cg + (int64_t)o.tx * p.V;
+    o.on = o.ty < p.ty && o.col < a.channels;
   }
-  __shared__ Moments s_m[kThreads / 32];
-  m = shfl_merge(m);
-  if ((threadIdx.x & 31) == 0) s_m[threadIdx.x >> 5] = m;
+  return o;
+}
+// Group `i` of the tile, among all (a.groups: none).
+__device__ __forceinline__ int64_t group_of(const NormArgs& a, const SlicePlan& p, const Place& o, int i) {
+  return p.pieces > 1 ? o.tile / p.pieces : (int64_t)o.tile * p.gpt + i;
+}
+
+// The rows of a thread, AHEAD at a time: load(u, at) of all of them, then use(u,
+// at) of each.  at: element of the thread's vector.
+template <int AHEAD, typename Load, typename Use>
+__device__ __forceinline__ void over_rows(const NormArgs& a, const SlicePlan& p, const Place& o,
+                                          Load&& load, Use&& use) {
+  const int64_t next = p.ty * a.channels;
+  int64_t at = (o.base + o.r0 + o.ty) * a.channels + o.col;
+  int left = o.r0 + o.ty < o.r1 ? ((int)(o.r1 - o.r0) - o.ty + p.ty - 1) / p.ty : 0;
+  for (; left >= AHEAD; left -= AHEAD) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) load(u, at + u * next);
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) use(u, at + u * next);
+    at += AHEAD * next;
+  }
+#pragma unroll
+  for (int u = 0; u < AHEAD - 1; ++u)
+    if (u < left) load(u, at + u * next);
+#pragma unroll
+  for (int u = 0; u < AHEAD - 1; ++u)
+    if (u < left) use(u, at + u * next);
+}
+
+// Sums over the threads of each group of the tile, a warp a group: f(group, sum).
+template <typename F>
+__device__ __forceinline__ void tile_sums(const SlicePlan& p, float2 c, float2* s_c, F&& f) {
+  s_c[threadIdx.x] = c;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kThreads / 32; ++i) m = merge(m, s_m[i]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wide = p.tx / p.gpt, count = wide * p.ty;
+  for (int i = warp; i < p.gpt; i += kThreads / 32) {
+    c = both(0.f);
+    if (p.ty == 1) {
+      for (int k = lane; k < wide; k += 32) c = fadd2(c, s_c[i * wide + k]);
+    } else {
+      for (int k = lane; k < count; k += 32) c = fadd2(c, s_c[(k / wide) * p.tx + i * wide + k % wide]);
+    }
+    c = make_float2(lane_sum(c.x, 32), lane_sum(c.y, 32));
+    if (lane == 0) f(i, c);
+  }
+}
+
+template <bool BF16, int V>
+__global__ void __launch_bounds__(kThreads, 4) slice_stats_kernel(const NormArgs a, const SlicePlan p) {
+  using X = Io<BF16, V>;
+  const Place o = place_of(a, p);
+  // sums about the group's first value in this split: it lies among the values,
+  // so the squares cannot be lost under it
+  float2 s1 = both(0.f), s2 = both(0.f);
+  auto pivot_of = [&](int64_t g) {
+    const int64_t at = (o.base + o.r0) * a.channels + g * a.cg;
+    return o.r0 < o.r1 ? io_load(a.x, at, BF16) : 0.f;
+  };
+  if (o.on) {
+    const float pivot = pivot_of(group_of(a, p, o, o.group));
+    typename X::R raw[kRowsAhead];
+    over_rows<kRowsAhead>(a, p, o, [&](int u, int64_t at) { raw[u] = X::load(a.x, at); },
+                          [&](int u, int64_t) {
+                            float2 f[X::P];
+                            X::unpack(raw[u], f);
+#pragma unroll
+                            for (int e = 0; e < X::P; ++e) {
+                              const float2 d = minus<V>(f[e], pivot);
+                              s1 = fadd2(s1, d);
+                              s2 = ffma2(d, d, s2);
+                            }
+                          });
+  }
+  __shared__ float2 s_c[kThreads];
+  tile_sums(p, make_float2(s1.x + s1.y, s2.x + s2.y), s_c, [&](int i, float2 c) {
+    const int64_t g = group_of(a, p, o, i);
+    if (g >= a.groups) return;
+    // values of the group in this block: its rows times its channels here
+    const int64_t nvec = a.cg / V, first = (int64_t)o.piece * p.tx;
+    const int64_t vecs = p.pieces > 1 ? (nvec - first < p.tx ? nvec - first : p.tx) : nvec;
+    const float n = (float)((o.r1 - o.r0) * vecs * V);
+    const float d = n > 0.f ? c.x / n : 0.f;
     Moments* out = reinterpret_cast<Moments*>(a.ws);
-    out[(int64_t)blockIdx.x * p.splits + blockIdx.y] = m;
-  }
+    out[((o.sample * a.groups + g) * p.splits + blockIdx.y) * p.pieces + o.piece] =
+        Moments{n, pivot_of(g) + d, fmaf(-d, c.x, c.y)};
+  });
 }
 
-template <bool BF16, int V>
-__global__ void __launch_bounds__(kThreads) slice_apply_kernel(const NormArgs a, const SlicePlan p) {
-  using X = Io<BF16, V>;
-  const int64_t sample = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
-  const Chain ch = rows_of(a, sample);
-  int64_t r0, r1;
-  split_rows(ch, p.splits, r0, r1);
-  __shared__ float s_stat[2];
-  if (threadIdx.x < 32) {  // the splits' moments, merged in the same order by every block
-    const Moments* in = reinterpret_cast<const Moments*>(a.ws) + (int64_t)blockIdx.x * p.splits;
-    Moments m{0.f, 0.f, 0.f};
-    for (int i = threadIdx.x; i < p.splits; i += 32) m = merge(m, in[i]);
-    m = shfl_merge(m);
-    if (threadIdx.x == 0) {
-      const float rstd = m.n > 0.f ? 1.f / sqrtf(m.m2 / m.n + a.eps) : 0.f;
-      s_stat[0] = m.mean;
-      s_stat[1] = rstd;
-      if (blockIdx.y == 0) {
-        if (a.mean) a.mean[blockIdx.x] = m.mean;
-        if (a.rstd) a.rstd[blockIdx.x] = rstd;
-      }
-    }
-  }
-  __syncthreads();
-  const float mean = s_stat[0], rstd = s_stat[1];
-  const int tx = threadIdx.x % p.tx, ty = threadIdx.x / p.tx;
-  const int64_t nvec = a.cg / V;
-  if (ty >= p.ty) return;
-  for (int64_t v = tx; v < nvec; v += p.tx) {
-    float w[V], b[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      w[e] = a.w ? __ldg(a.w + g * a.cg + v * V + e) : 1.f;
-      b[e] = a.b ? __ldg(a.b + g * a.cg + v * V + e) : 0.f;
-    }
-    for (int64_t r = r0 + ty; r < r1; r += p.ty) {
-      const int64_t at = (ch.base + r) * a.channels + g * a.cg + v * V;
-      float x[V], z[V], o[V];
-      X::unpack(X::load(a.x, at), x);
-      if (a.act == M3_ACT_GATE) X::unpack(X::load(a.z, at), z);
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        o[e] = activate(a.act, fmaf((x[e] - mean) * rstd, w[e], b[e]), z[e]);
-      if (M3_IN(at + V - 1, a.total_tokens * a.channels, a.status)) X::store(a.y, at, o);
-    }
-  }
-}
-
-// Backward, first pass: the slice's two sums (one partial per split) and the
-// block's share of dw, db (one row of partials per sample and split), and dz.
-template <bool BF16, int V>
+// A slice's mean and 1 / deviation from its partial moments, a warp each.
 __global__ void __launch_bounds__(kThreads)
+slice_finish_kernel(const NormArgs a, int parts, int64_t slices, float2* stat) {
+  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (i >= slices) return;
+  const Moments* in = reinterpret_cast<const Moments*>(a.ws) + i * parts;
+  Moments m{0.f, 0.f, 0.f};
+  for (int k = lane; k < parts; k += 32) m = merge(m, in[k]);
+  m = shfl_merge(m);
+  if (lane != 0) return;
+  const float rstd = m.n > 0.f ? rsqrtf(m.m2 / m.n + a.eps) : 0.f;
+  stat[i] = make_float2(m.mean, rstd);
+  if (a.mean) a.mean[i] = m.mean;
+  if (a.rstd) a.rstd[i] = rstd;
+}
+
+template <bool BF16, int V, int ACT>
+__global__ void __launch_bounds__(kThreads, 4)
+slice_apply_kernel(const NormArgs a, const SlicePlan p, const float2* stat) {
+  using X = Io<BF16, V>;
+  const Place o = place_of(a, p);
+  if (!o.on) return;
+  const float2 st = stat[o.sample * a.groups + group_of(a, p, o, o.group)];
+  const float mean = st.x;
+  float2 w[X::P], b[X::P];
+  load_params<V>(a, o.col, true, w, b);
+#pragma unroll
+  for (int e = 0; e < X::P; ++e) w[e] = fmul2(w[e], both(st.y));
+  typename X::R xr[kRowsAhead], zr[kRowsAhead];
+  over_rows<kRowsAhead>(a, p, o,
+            [&](int u, int64_t at) {
+              xr[u] = X::load(a.x, at);
+              if constexpr (ACT == M3_ACT_GATE) zr[u] = X::load(a.z, at);
+            },
+            [&](int u, int64_t at) {
+              float2 x[X::P], z[X::P], y[X::P];
+              X::unpack(xr[u], x);
+              if constexpr (ACT == M3_ACT_GATE) X::unpack(zr[u], z);
+#pragma unroll
+              for (int e = 0; e < X::P; ++e)
+                y[e] = activate<ACT>(ffma2(minus<V>(x[e], mean), w[e], b[e]), z[e]);
+              if (M3_IN(at + V - 1, a.total_tokens * a.channels, a.status)) X::store(a.y, at, y);
+            });
+}
+
+// Backward, first pass: the groups' two sums (one partial per split and piece),
+// the block's share of dw, db (one row of partials per sample and split), and dz.
+template <bool BF16, int V, int ACT>
+__global__ void __launch_bounds__(kThreads, 3)
 slice_sums_kernel(const NormArgs a, const SlicePlan p, float2* csum, float* part) {
   using X = Io<BF16, V>;
-  const int64_t sample = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
-  const Chain ch = rows_of(a, sample);
-  int64_t r0, r1;
-  split_rows(ch, p.splits, r0, r1);
-  const int tx = threadIdx.x % p.tx, ty = threadIdx.x / p.tx;
-  const int64_t nvec = a.cg / V;
-  const float mean = __ldg(a.mean + blockIdx.x), rstd = __ldg(a.rstd + blockIdx.x);
-  const int64_t prow = sample * p.splits + blockIdx.y, prows = a.batch * p.splits;
-  extern __shared__ float s_col[];  // [2][ty][tx * V]
-  float c1 = 0.f, c2 = 0.f;
-  for (int64_t v0 = 0; v0 < nvec; v0 += p.tx) {
-    const int64_t v = v0 + tx;
-    const bool on = ty < p.ty && v < nvec;
-    float dw[V], db[V];
+  const Place o = place_of(a, p);
+  float2 c = both(0.f), dw[X::P], db[X::P];
 #pragma unroll
-    for (int e = 0; e < V; ++e) dw[e] = db[e] = 0.f;
-    if (on) {
-      float w[V], b[V];
+  for (int e = 0; e < X::P; ++e) dw[e] = db[e] = both(0.f);
+  if (o.on) {
+    const int64_t g = o.sample * a.groups + group_of(a, p, o, o.group);
+    const float mean = __ldg(a.mean + g), rstd = __ldg(a.rstd + g);
+    float2 w[X::P], b[X::P];
+    load_params<V>(a, o.col, true, w, b);
+    typename X::R xr[kBwdRowsAhead], yr[kBwdRowsAhead], zr[kBwdRowsAhead];
+    over_rows<kBwdRowsAhead>(a, p, o,
+              [&](int u, int64_t at) {
+                xr[u] = X::load(a.x, at);
+                yr[u] = X::load(a.dy, at);
+                if constexpr (ACT == M3_ACT_GATE) zr[u] = X::load(a.z, at);
+              },
+              [&](int u, int64_t at) {
+                float2 x[X::P], dy[X::P], z[X::P], dz[X::P];
+                X::unpack(xr[u], x);
+                X::unpack(yr[u], dy);
+                if constexpr (ACT == M3_ACT_GATE) X::unpack(zr[u], z);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        w[e] = a.w ? __ldg(a.w + g * a.cg + v * V + e) : 1.f;
-        b[e] = a.b ? __ldg(a.b + g * a.cg + v * V + e) : 0.f;
-      }
-      for (int64_t r = r0 + ty; r < r1; r += p.ty) {
-        const int64_t at = (ch.base + r) * a.channels + g * a.cg + v * V;
-        float x[V], dy[V], z[V], dz[V];
-        X::unpack(X::load(a.x, at), x);
-        X::unpack(X::load(a.dy, at), dy);
-        if (a.act == M3_ACT_GATE) X::unpack(X::load(a.z, at), z);
+                for (int e = 0; e < X::P; ++e) {
+                  const float2 xh = fmul2(minus<V>(x[e], mean), both(rstd));
+                  const float2 gr = act_grad<ACT>(ffma2(xh, w[e], b[e]), z[e], dy[e], dz[e]);
+                  dw[e] = ffma2(gr, xh, dw[e]);
+                  db[e] = fadd2(db[e], gr);
+                }
+                if (ACT == M3_ACT_GATE && a.dz &&
+                    M3_IN(at + V - 1, a.total_tokens * a.channels, a.status))
+                  X::store(a.dz, at, dz);
+              });
+    // a channel's weight is the same in all its rows
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float xh = (x[e] - mean) * rstd;
-          const float gr = act_grad(a.act, fmaf(xh, w[e], b[e]), z[e], dy[e], dz[e]);
-          dw[e] = fmaf(gr, xh, dw[e]);
-          db[e] += gr;
-          c1 = fmaf(gr, w[e], c1);
-          c2 = fmaf(gr * w[e], xh, c2);
-        }
-        if (a.act == M3_ACT_GATE && a.dz && M3_IN(at + V - 1, a.total_tokens * a.channels, a.status))
-          X::store(a.dz, at, dz);
-      }
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        s_col[(ty * p.tx + tx) * V + e] = dw[e];
-        s_col[((p.ty + ty) * p.tx + tx) * V + e] = db[e];
-      }
+    for (int e = 0; e < X::P; ++e) {
+      c.x += db[e].x * w[e].x + db[e].y * w[e].y;
+      c.y += dw[e].x * w[e].x + dw[e].y * w[e].y;
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.tx * V; i += kThreads) {
-      const int64_t c = v0 * V + i;
-      if (c >= a.cg) break;
-      float tw = 0.f, tb = 0.f;
-      for (int r = 0; r < p.ty; ++r) {
-        tw += s_col[r * p.tx * V + i];
-        tb += s_col[(p.ty + r) * p.tx * V + i];
-      }
-      part[prow * a.channels + g * a.cg + c] = tw;
-      part[(prows + prow) * a.channels + g * a.cg + c] = tb;
-    }
-    __syncthreads();
   }
-  __shared__ float2 s_c[kThreads / 32];
-  c1 = lane_sum(c1, 32);
-  c2 = lane_sum(c2, 32);
-  if ((threadIdx.x & 31) == 0) s_c[threadIdx.x >> 5] = make_float2(c1, c2);
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kThreads / 32; ++i) {
-      c1 += s_c[i].x;
-      c2 += s_c[i].y;
+  __shared__ float2 s_c[kThreads];
+  extern __shared__ float s_col[];  // [2][ty][tx * V], for dw and db
+  const int width = p.tx * V;
+  if (part && o.ty < p.ty) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      s_col[o.ty * width + o.tx * V + e] = (e & 1) ? dw[e / 2].y : dw[e / 2].x;
+      s_col[(p.ty + o.ty) * width + o.tx * V + e] = (e & 1) ? db[e / 2].y : db[e / 2].x;
     }
-    csum[(int64_t)blockIdx.x * p.splits + blockIdx.y] = make_float2(c1, c2);
   }
+  tile_sums(p, c, s_c, [&](int i, float2 v) {
+    const int64_t g = group_of(a, p, o, i);
+    if (g < a.groups)
+      csum[((o.sample * a.groups + g) * p.splits + blockIdx.y) * p.pieces + o.piece] = v;
+  });
+  if (!part) return;
+  // columns of the tile: the first of its channels, and how many there are
+  const int64_t c0 = o.col - (int64_t)o.tx * V;
+  const int64_t end = p.pieces > 1 ? (o.tile / p.pieces + 1) * a.cg : a.channels;
+  const int64_t prow = o.sample * p.splits + blockIdx.y, prows = a.batch * p.splits;
+  for (int i = threadIdx.x; i < 2 * width; i += kThreads) {
+    const int which = i >= width, j = i - which * width;
+    if (c0 + j >= end) continue;
+    float v = 0.f;
+    for (int r = 0; r < p.ty; ++r) v += s_col[(which * p.ty + r) * width + j];
+    part[(which * prows + prow) * a.channels + c0 + j] = v;
+  }
+}
+
+// A slice's two means from its partial sums, a warp each.
+__global__ void __launch_bounds__(kThreads)
+slice_means_kernel(const NormArgs a, int parts, int64_t slices, const float2* csum, float2* means) {
+  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (i >= slices) return;
+  float2 c = both(0.f);
+  for (int k = lane; k < parts; k += 32) c = fadd2(c, csum[i * parts + k]);
+  c = make_float2(lane_sum(c.x, 32), lane_sum(c.y, 32));
+  const float n = (float)((double)rows_of(a, i / a.groups).len * (double)a.cg);
+  if (lane == 0) means[i] = make_float2(c.x / n, c.y / n);
 }
 
 // Backward, second pass: dx.
-template <bool BF16, int V>
-__global__ void __launch_bounds__(kThreads)
-slice_dx_kernel(const NormArgs a, const SlicePlan p, const float2* csum) {
+template <bool BF16, int V, int ACT>
+__global__ void __launch_bounds__(kThreads, 3)
+slice_dx_kernel(const NormArgs a, const SlicePlan p, const float2* means) {
   using X = Io<BF16, V>;
-  const int64_t sample = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
-  const Chain ch = rows_of(a, sample);
-  int64_t r0, r1;
-  split_rows(ch, p.splits, r0, r1);
-  __shared__ float2 s_c;
-  if (threadIdx.x < 32) {
-    float c1 = 0.f, c2 = 0.f;
-    for (int i = threadIdx.x; i < p.splits; i += 32) {
-      const float2 c = csum[(int64_t)blockIdx.x * p.splits + i];
-      c1 += c.x;
-      c2 += c.y;
-    }
-    c1 = lane_sum(c1, 32);
-    c2 = lane_sum(c2, 32);
-    const float n = (float)((double)ch.len * (double)a.cg);
-    if (threadIdx.x == 0) s_c = make_float2(c1 / n, c2 / n);
-  }
-  __syncthreads();
-  const float c1 = s_c.x, c2 = s_c.y;
-  const float mean = __ldg(a.mean + blockIdx.x), rstd = __ldg(a.rstd + blockIdx.x);
-  const int tx = threadIdx.x % p.tx, ty = threadIdx.x / p.tx;
-  const int64_t nvec = a.cg / V;
-  if (ty >= p.ty) return;
-  for (int64_t v = tx; v < nvec; v += p.tx) {
-    float w[V], b[V];
+  const Place o = place_of(a, p);
+  if (!o.on) return;
+  const int64_t g = o.sample * a.groups + group_of(a, p, o, o.group);
+  const float mean = __ldg(a.mean + g), rstd = __ldg(a.rstd + g);
+  const float2 c = means[g], k1 = both(-c.x * rstd), k2 = both(-c.y * rstd);
+  float2 w[X::P], b[X::P];
+  load_params<V>(a, o.col, true, w, b);
+  typename X::R xr[kBwdRowsAhead], yr[kBwdRowsAhead], zr[kBwdRowsAhead];
+  over_rows<kBwdRowsAhead>(a, p, o,
+            [&](int u, int64_t at) {
+              xr[u] = X::load(a.x, at);
+              yr[u] = X::load(a.dy, at);
+              if constexpr (ACT == M3_ACT_GATE) zr[u] = X::load(a.z, at);
+            },
+            [&](int u, int64_t at) {
+              float2 x[X::P], dy[X::P], z[X::P], dx[X::P], dz;
+              X::unpack(xr[u], x);
+              X::unpack(yr[u], dy);
+              if constexpr (ACT == M3_ACT_GATE) X::unpack(zr[u], z);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      w[e] = a.w ? __ldg(a.w + g * a.cg + v * V + e) : 1.f;
-      b[e] = a.b ? __ldg(a.b + g * a.cg + v * V + e) : 0.f;
-    }
-    for (int64_t r = r0 + ty; r < r1; r += p.ty) {
-      const int64_t at = (ch.base + r) * a.channels + g * a.cg + v * V;
-      float x[V], dy[V], z[V], o[V], dz;
-      X::unpack(X::load(a.x, at), x);
-      X::unpack(X::load(a.dy, at), dy);
-      if (a.act == M3_ACT_GATE) X::unpack(X::load(a.z, at), z);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float xh = (x[e] - mean) * rstd;
-        const float gr = act_grad(a.act, fmaf(xh, w[e], b[e]), z[e], dy[e], dz);
-        o[e] = rstd * (gr * w[e] - c1 - xh * c2);
-      }
-      if (M3_IN(at + V - 1, a.total_tokens * a.channels, a.status)) X::store(a.dx, at, o);
-    }
-  }
+              for (int e = 0; e < X::P; ++e) {
+                const float2 xh = fmul2(minus<V>(x[e], mean), both(rstd));
+                const float2 gr = act_grad<ACT>(ffma2(xh, w[e], b[e]), z[e], dy[e], dz);
+                dx[e] = ffma2(fmul2(gr, w[e]), both(rstd), ffma2(xh, k2, k1));
+              }
+              if (M3_IN(at + V - 1, a.total_tokens * a.channels, a.status)) X::store(a.dx, at, dx);
+            });
 }
 
-// dw, db: the rows of partials added in a fixed order.  32 channels a block.
+// dw (blockIdx.y = 0) or db: the rows of partials added in a fixed order, 32
+// channels a block.
 __global__ void __launch_bounds__(1024)
-param_reduce_kernel(const float* part, int64_t rows, int64_t channels, float* dw, float* db) {
-  __shared__ float s[2][32][33];
+param_reduce_kernel(const float* part, int rows, int64_t channels, float* dw, float* db) {
+  __shared__ float s[32][33];
+  float* out = blockIdx.y == 0 ? dw : db;
+  if (!out) return;
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + cx;
-  float tw = 0.f, tb = 0.f;
+  float t = 0.f;
   if (c < channels) {
-    for (int64_t r = ry; r < rows; r += 32) {
-      tw += part[r * channels + c];
-      tb += part[(rows + r) * channels + c];
-    }
+    const float* p = part + ((int64_t)blockIdx.y * rows + ry) * channels + c;
+#pragma unroll 8
+    for (int r = ry; r < rows; r += 32, p += 32 * channels) t += *p;
   }
-  s[0][ry][cx] = tw;
-  s[1][ry][cx] = tb;
+  s[ry][cx] = t;
   __syncthreads();
-  if (ry < 2) {  // warp 0 adds dw's column sums, warp 1 db's
-    float t = 0.f;
+  if (ry == 0 && c < channels) {
+    t = 0.f;
 #pragma unroll
-    for (int r = 0; r < 32; ++r) t += s[ry][r][cx];
-    float* out = ry == 0 ? dw : db;
-    if (out && c < channels) out[c] = t;
+    for (int r = 0; r < 32; ++r) t += s[r][cx];
+    out[c] = t;
   }
 }
 
@@ -608,10 +825,16 @@ bool unit_plan(const NormArgs& a, bool backward, UnitPlan* p) {
   if (a.seqlen != 1 || a.cu_seqlens) return false;
   p->V = vec_elems(a);
   const int64_t nvec = a.cg / p->V;
+  // up to 32 lanes a vector each, then several vectors a lane, then several warps
   int L = 1;
   while (L < 32 && L < nvec) L <<= 1;
+  auto fits = [&](int lanes) {
+    const int64_t n = (nvec + lanes - 1) / lanes;
+    return n <= 16 && round_nv(n) * p->V <= kMaxLaneElems;
+  };
+  while (L < kThreads && !fits(L)) L <<= 1;
+  if (!fits(L)) return false;
   const int64_t nv = (nvec + L - 1) / L;
-  if (nv > 16 || round_nv(nv) * p->V > kMaxLaneElems) return false;
   p->L = L;
   p->NV = round_nv(nv);
   const int slots = kThreads / L;
@@ -629,15 +852,28 @@ bool unit_plan(const NormArgs& a, bool backward, UnitPlan* p) {
   return true;
 }
 
-SlicePlan slice_plan(const NormArgs& a) {
+SlicePlan slice_plan(const NormArgs& a, bool backward) {
   SlicePlan p;
   p.V = vec_elems(a);
   const int64_t nvec = a.cg / p.V;
-  p.tx = (int)(nvec < kThreads ? nvec : kThreads);
+  p.pieces = (int)((nvec + kThreads - 1) / kThreads);
+  if (p.pieces > 1) {
+    p.gpt = 1;
+    p.tx = kThreads;
+    p.tiles = (int)(a.groups * p.pieces);
+  } else {
+    const int64_t fit = kThreads / nvec;
+    p.tiles = (int)((a.groups + fit - 1) / fit);
+    p.gpt = (int)((a.groups + p.tiles - 1) / p.tiles);
+    p.tx = (int)(p.gpt * nvec);
+    p.tiles = (int)((a.groups + p.gpt - 1) / p.gpt);
+  }
   p.ty = kThreads / p.tx;
-  const int64_t slices = a.batch * a.groups;
-  int64_t s = ((int64_t)kPlanSms * 8 + slices - 1) / slices;
-  const int64_t most = (a.seqlen + 4 * p.ty - 1) / (4 * p.ty);  // at least four rows a thread
+  const int64_t blocks = a.batch * p.tiles;
+  // as many blocks as run at one time (three an SM in the backward, whose threads
+  // hold more), so that each has many rows to spread its start and end over
+  int64_t s = (int64_t)kPlanSms * (backward ? 3 : 4) / blocks;
+  const int64_t most = (a.seqlen + kRowsAhead * p.ty - 1) / (kRowsAhead * p.ty);
   if (s > most) s = most;
   if (s > 1024) s = 1024;
   p.splits = (int)(s < 1 ? 1 : s);
@@ -648,72 +884,96 @@ size_t unit_bwd_bytes(const NormArgs& a, const UnitPlan& p) {
   return (size_t)2 * p.yb * a.channels * 4;
 }
 
-size_t slice_csum_bytes(const NormArgs& a, const SlicePlan& p) {
-  return align_up((size_t)a.batch * a.groups * p.splits * sizeof(float2), 256);
+size_t slice_stat_bytes(const NormArgs& a) {
+  return align_up((size_t)a.batch * a.groups * sizeof(float2), 256);
 }
 
-#define M3_NORM_V(KERNEL, V, ...)                                \
-  do {                                                           \
-    if (a.bf16) {                                                \
-      switch (V) {                                               \
-        case 8: KERNEL<true, 8> __VA_ARGS__; break;              \
-        case 4: KERNEL<true, 4> __VA_ARGS__; break;              \
-        case 2: KERNEL<true, 2> __VA_ARGS__; break;              \
-        default: KERNEL<true, 1> __VA_ARGS__; break;             \
-      }                                                          \
-    } else {                                                     \
-      switch (V) {                                               \
-        case 4: KERNEL<false, 4> __VA_ARGS__; break;             \
-        case 2: KERNEL<false, 2> __VA_ARGS__; break;             \
-        default: KERNEL<false, 1> __VA_ARGS__; break;            \
-      }                                                          \
-    }                                                            \
-  } while (0)
+size_t slice_csum_bytes(const NormArgs& a, const SlicePlan& p) {
+  return align_up((size_t)a.batch * a.groups * p.splits * p.pieces * sizeof(float2), 256);
+}
 
-template <bool BF16, int V, int NV>
-cudaError_t unit_launch_nv(const NormArgs& a, const UnitPlan& p, bool backward, cudaStream_t s) {
-  const dim3 grid((unsigned)p.xb, (unsigned)p.yb);
-  if constexpr (V * NV <= kMaxLaneElems) {
-    if (backward) {
-      const size_t smem = a.ws ? (size_t)2 * p.ty * p.ub * a.cg * 4 : 0;
-      if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(unit_bwd_kernel<BF16, V, NV>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-      }
-      unit_bwd_kernel<BF16, V, NV><<<grid, kThreads, smem, s>>>(a, p);
-    } else {
-      unit_fwd_kernel<BF16, V, NV><<<grid, kThreads, 0, s>>>(a, p);
+// f(bf16, vector elements, activation) as compile-time constants
+template <typename F>
+cudaError_t with_shape(const NormArgs& a, int V, F&& f) {
+  auto act = [&](auto bf16, auto v) {
+    switch (a.act) {
+      case M3_ACT_SILU: return f(bf16, v, std::integral_constant<int, M3_ACT_SILU>());
+      case M3_ACT_GATE: return f(bf16, v, std::integral_constant<int, M3_ACT_GATE>());
+      default: return f(bf16, v, std::integral_constant<int, M3_ACT_NONE>());
+    }
+  };
+  if (a.bf16) {
+    switch (V) {
+      case 8: return act(std::true_type(), std::integral_constant<int, 8>());
+      case 4: return act(std::true_type(), std::integral_constant<int, 4>());
+      case 2: return act(std::true_type(), std::integral_constant<int, 2>());
+      default: return act(std::true_type(), std::integral_constant<int, 1>());
     }
   }
+  switch (V) {
+    case 4: return act(std::false_type(), std::integral_constant<int, 4>());
+    case 2: return act(std::false_type(), std::integral_constant<int, 2>());
+    default: return act(std::false_type(), std::integral_constant<int, 1>());
+  }
+}
+
+template <typename K, typename... Args>
+cudaError_t launch(K kernel, dim3 grid, size_t smem, cudaStream_t s, Args... args) {
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<grid, kThreads, smem, s>>>(args...);
   return cudaGetLastError();
 }
 
-template <bool BF16, int V>
-cudaError_t unit_launch_v(const NormArgs& a, const UnitPlan& p, bool backward, cudaStream_t s) {
-  switch (p.NV) {
-    case 1: return unit_launch_nv<BF16, V, 1>(a, p, backward, s);
-    case 2: return unit_launch_nv<BF16, V, 2>(a, p, backward, s);
-    case 4: return unit_launch_nv<BF16, V, 4>(a, p, backward, s);
-    case 8: return unit_launch_nv<BF16, V, 8>(a, p, backward, s);
-    default: return unit_launch_nv<BF16, V, 16>(a, p, backward, s);
+// The lanes of a unit are a compile-time number where the vectors are whole
+// 16 bytes of 64 or 128 channels (8 or 16 lanes) and where there are 32.
+template <bool BF16, int V, int NV, int ACT>
+cudaError_t unit_launch_nv(const NormArgs& a, const UnitPlan& p, bool backward, cudaStream_t s) {
+  const dim3 grid((unsigned)p.xb, (unsigned)p.yb);
+  if constexpr (V * NV > kMaxLaneElems) return cudaErrorInvalidValue;
+  else {
+    const size_t smem = backward && a.ws ? (size_t)2 * p.ty * p.ub * a.cg * 4 : 0;
+    constexpr int wide = V * (BF16 ? 2 : 4) == 16;
+    auto go = [&](auto lanes) {
+      constexpr int L = decltype(lanes)::value;
+      return backward ? launch(unit_bwd_kernel<BF16, V, NV, L, ACT>, grid, smem, s, a, p)
+                      : launch(unit_fwd_kernel<BF16, V, NV, L, ACT>, grid, 0, s, a, p);
+    };
+    if (p.L == 32) return go(std::integral_constant<int, 32>());
+    if constexpr (V * NV > kMaxLaneElems / 4) {  // more lanes only where fewer would hold too much
+      if (p.L > 32) return go(std::integral_constant<int, -1>());
+    }
+    if constexpr (NV == 1) {
+      if constexpr (wide) {
+        if (p.L == 8) return go(std::integral_constant<int, 8>());
+        if (p.L == 16) return go(std::integral_constant<int, 16>());
+      }
+      return go(std::integral_constant<int, 0>());
+    }
+    return cudaErrorInvalidValue;  // several vectors a lane only with 32 lanes
   }
 }
 
 cudaError_t unit_launch(const NormArgs& a, const UnitPlan& p, bool backward, cudaStream_t s) {
-  if (a.bf16) {
-    switch (p.V) {
-      case 8: return unit_launch_v<true, 8>(a, p, backward, s);
-      case 4: return unit_launch_v<true, 4>(a, p, backward, s);
-      case 2: return unit_launch_v<true, 2>(a, p, backward, s);
-      default: return unit_launch_v<true, 1>(a, p, backward, s);
+  return with_shape(a, p.V, [&](auto bf16, auto v, auto act) {
+    constexpr bool B = decltype(bf16)::value;
+    constexpr int V = decltype(v)::value, A = decltype(act)::value;
+    switch (p.NV) {
+      case 1: return unit_launch_nv<B, V, 1, A>(a, p, backward, s);
+      case 2: return unit_launch_nv<B, V, 2, A>(a, p, backward, s);
+      case 4: return unit_launch_nv<B, V, 4, A>(a, p, backward, s);
+      case 8: return unit_launch_nv<B, V, 8, A>(a, p, backward, s);
+      default: return unit_launch_nv<B, V, 16, A>(a, p, backward, s);
     }
-  }
-  switch (p.V) {
-    case 4: return unit_launch_v<false, 4>(a, p, backward, s);
-    case 2: return unit_launch_v<false, 2>(a, p, backward, s);
-    default: return unit_launch_v<false, 1>(a, p, backward, s);
-  }
+  });
+}
+
+cudaError_t param_reduce(const NormArgs& a, const float* part, int64_t rows, cudaStream_t s) {
+  param_reduce_kernel<<<dim3((unsigned)((a.channels + 31) / 32), 2), 1024, 0, s>>>(
+      part, (int)rows, a.channels, a.dw, a.db);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -721,22 +981,29 @@ cudaError_t unit_launch(const NormArgs& a, const UnitPlan& p, bool backward, cud
 size_t group_norm_workspace(const NormArgs& a, bool backward) {
   UnitPlan u;
   if (unit_plan(a, backward, &u)) return backward ? unit_bwd_bytes(a, u) : 0;
-  const SlicePlan p = slice_plan(a);
-  const size_t slices = (size_t)a.batch * a.groups * p.splits;
-  if (!backward) return slices * sizeof(Moments);
-  return slice_csum_bytes(a, p) + (size_t)2 * a.batch * p.splits * a.channels * 4;
+  const SlicePlan p = slice_plan(a, backward);
+  if (!backward) return slice_stat_bytes(a) + (size_t)a.batch * a.groups * p.splits * p.pieces * sizeof(Moments);
+  return slice_stat_bytes(a) + slice_csum_bytes(a, p) + (size_t)2 * a.batch * p.splits * a.channels * 4;
 }
 
-cudaError_t group_norm_fwd_launch(const NormArgs& a, cudaStream_t s) {
+cudaError_t group_norm_fwd_launch(const NormArgs& a0, cudaStream_t s) {
+  NormArgs a = a0;
   UnitPlan u;
   if (unit_plan(a, false, &u)) return unit_launch(a, u, false, s);
-  const SlicePlan p = slice_plan(a);
-  const dim3 grid((unsigned)(a.batch * a.groups), (unsigned)p.splits);
-  M3_NORM_V(slice_stats_kernel, p.V, <<<grid, kThreads, 0, s>>>(a, p));
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  M3_NORM_V(slice_apply_kernel, p.V, <<<grid, kThreads, 0, s>>>(a, p));
-  return cudaGetLastError();
+  const SlicePlan p = slice_plan(a, false);
+  const dim3 grid((unsigned)(a.batch * p.tiles), (unsigned)p.splits);
+  const int64_t slices = a.batch * a.groups;
+  float2* stat = reinterpret_cast<float2*>(a.ws);
+  a.ws += slice_stat_bytes(a);
+  return with_shape(a, p.V, [&](auto bf16, auto v, auto act) {
+    constexpr bool B = decltype(bf16)::value;
+    constexpr int V = decltype(v)::value, A = decltype(act)::value;
+    cudaError_t e = launch(slice_stats_kernel<B, V>, grid, 0, s, a, p);
+    if (e == cudaSuccess)
+      e = launch(slice_finish_kernel, dim3((unsigned)((slices + kThreads / 32 - 1) / (kThreads / 32))), 0, s,
+                 a, p.splits * p.pieces, slices, stat);
+    return e != cudaSuccess ? e : launch(slice_apply_kernel<B, V, A>, grid, 0, s, a, p, (const float2*)stat);
+  });
 }
 
 cudaError_t group_norm_bwd_launch(const NormArgs& a0, cudaStream_t s) {
@@ -744,33 +1011,28 @@ cudaError_t group_norm_bwd_launch(const NormArgs& a0, cudaStream_t s) {
   UnitPlan u;
   const bool params = a.dw || a.db;
   if (unit_plan(a, true, &u)) {
-    char* ws = a.ws;
+    const float* part = reinterpret_cast<const float*>(a.ws);
     if (!params) a.ws = nullptr;
-    cudaError_t e = unit_launch(a, u, true, s);
-    if (e != cudaSuccess || !params) return e;
-    param_reduce_kernel<<<(unsigned)((a.channels + 31) / 32), 1024, 0, s>>>(
-        reinterpret_cast<const float*>(ws), u.yb, a.channels, a.dw, a.db);
-    return cudaGetLastError();
+    const cudaError_t e = unit_launch(a, u, true, s);
+    return e != cudaSuccess || !params ? e : param_reduce(a, part, u.yb, s);
   }
-  const SlicePlan p = slice_plan(a);
-  const dim3 grid((unsigned)(a.batch * a.groups), (unsigned)p.splits);
-  float2* csum = reinterpret_cast<float2*>(a.ws);
-  float* part = reinterpret_cast<float*>(a.ws + slice_csum_bytes(a, p));
-  const size_t smem = (size_t)2 * p.ty * p.tx * p.V * 4;
-  M3_NORM_V(slice_sums_kernel, p.V, <<<grid, kThreads, smem, s>>>(a, p, csum, part));
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  if (a.dx) {
-    M3_NORM_V(slice_dx_kernel, p.V, <<<grid, kThreads, 0, s>>>(a, p, csum));
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  if (params) {
-    param_reduce_kernel<<<(unsigned)((a.channels + 31) / 32), 1024, 0, s>>>(
-        part, a.batch * p.splits, a.channels, a.dw, a.db);
-    e = cudaGetLastError();
-  }
-  return e;
+  const SlicePlan p = slice_plan(a, true);
+  const dim3 grid((unsigned)(a.batch * p.tiles), (unsigned)p.splits);
+  const int64_t slices = a.batch * a.groups;
+  float2* means = reinterpret_cast<float2*>(a.ws);
+  float2* csum = reinterpret_cast<float2*>(a.ws + slice_stat_bytes(a));
+  float* rows = params ? reinterpret_cast<float*>(a.ws + slice_stat_bytes(a) + slice_csum_bytes(a, p)) : nullptr;
+  const size_t smem = params ? (size_t)2 * p.ty * p.tx * p.V * 4 : 0;
+  const cudaError_t e = with_shape(a, p.V, [&](auto bf16, auto v, auto act) {
+    constexpr bool B = decltype(bf16)::value;
+    constexpr int V = decltype(v)::value, A = decltype(act)::value;
+    cudaError_t r = launch(slice_sums_kernel<B, V, A>, grid, smem, s, a, p, csum, rows);
+    if (r != cudaSuccess || !a.dx) return r;
+    r = launch(slice_means_kernel, dim3((unsigned)((slices + kThreads / 32 - 1) / (kThreads / 32))), 0, s, a,
+               p.splits * p.pieces, slices, (const float2*)csum, means);
+    return r != cudaSuccess ? r : launch(slice_dx_kernel<B, V, A>, grid, 0, s, a, p, (const float2*)means);
+  });
+  return e != cudaSuccess || !params ? e : param_reduce(a, rows, a.batch * p.splits, s);
 }
 
 }  // namespace m3
