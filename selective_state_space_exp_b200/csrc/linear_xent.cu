@@ -398,48 +398,45 @@ xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
   }
 }
 
-// Joins the tiles' maxima and sums of a token: 32 tokens a block, 8 warps over
-// the tiles.
-__global__ void __launch_bounds__(256)
+// (maximum, sum) of the exponentials of two sets.
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  const float nm = fmaxf(a.x, b.x);
+  // both sets -infinity only: their sums hold 0 or NaN
+  return nm > -INFINITY ? make_float2(nm, a.y * ex2(a.x - nm) + b.y * ex2(b.x - nm))
+                        : make_float2(nm, a.y + b.y);
+}
+
+// Joins the tiles' maxima and sums of a token: kJoinTokens tokens a block, the
+// other threads over the tiles.
+constexpr int kJoinTokens = 8, kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads)
 xent_join_kernel(const float2* stat, int parts, int64_t M, int64_t V, const int64_t* targets,
                  int64_t ignore, const float* tlogit, float* loss, float* lse, int* status) {
-  __shared__ float2 s[8][32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t m = (int64_t)blockIdx.x * 32 + lane;
-  float mx = -INFINITY, sum = 0.f;
+  constexpr int kRows = kJoinThreads / kJoinTokens;
+  __shared__ float2 s[kRows][kJoinTokens];
+  const int t = threadIdx.x % kJoinTokens, w = threadIdx.x / kJoinTokens;
+  const int64_t m = (int64_t)blockIdx.x * kJoinTokens + t;
+  float2 v = make_float2(-INFINITY, 0.f);
   if (m < M) {
-    for (int p = w; p < parts; p += 8) {
-      const float2 v = stat[(int64_t)p * M + m];
-      const float nm = fmaxf(mx, v.x);
-      if (nm > -INFINITY) {
-        sum = sum * ex2(mx - nm) + v.y * ex2(v.x - nm);
-        mx = nm;
-      } else {
-        sum += v.y;
-      }
-    }
+#pragma unroll 4
+    for (int p = w; p < parts; p += kRows) v = join(v, stat[(int64_t)p * M + m]);
   }
-  s[w][lane] = make_float2(mx, sum);
+  s[w][t] = v;
   __syncthreads();
-  if (w != 0 || m >= M) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    const float2 v = s[i][lane];
-    const float nm = fmaxf(mx, v.x);
-    if (nm > -INFINITY) {
-      sum = sum * ex2(mx - nm) + v.y * ex2(v.x - nm);
-      mx = nm;
-    } else {
-      sum += v.y;
-    }
+  for (int h = kRows / 2; h > 0; h >>= 1) {  // a tree of fixed order
+    if (w < h) s[w][t] = join(s[w][t], s[w + h][t]);
+    __syncthreads();
   }
-  const float z = (mx + log2f(sum)) * kLn2;
+  if (w != 0 || m >= M) return;
+  v = s[0][t];
+  const float z = (v.x + log2f(v.y)) * kLn2;
   if (lse) lse[m] = z;
   if (!loss) return;
-  const int64_t t = targets[m];
-  if (t == ignore) {
+  const int64_t y = targets[m];
+  if (y == ignore) {
     loss[m] = 0.f;
-  } else if (t < 0 || t >= V) {
+  } else if (y < 0 || y >= V) {
     if (status) atomicCAS(status, 0, (int)M3_ERR_INVALID_ARGUMENT);
     loss[m] = __int_as_float(0x7fffffff);  // NaN
   } else {
@@ -605,7 +602,7 @@ cudaError_t xent_fwd_launch(const XentArgs& a, cudaStream_t s) {
   cudaError_t e = gemm<kStats, false, false>(g, Operand{a.h, a.M, a.K, a.K},
                                              Operand{a.W, a.V, a.K, a.K}, s);
   if (e != cudaSuccess) return e;
-  xent_join_kernel<<<(unsigned)ceil_div(a.M, 32), 256, 0, s>>>(
+  xent_join_kernel<<<(unsigned)ceil_div(a.M, kJoinTokens), kJoinThreads, 0, s>>>(
       g.stat, 2 * g.nt, a.M, a.V, a.targets, a.ignore, g.tlogit, a.loss, a.lse, a.status);
   return cudaGetLastError();
 }

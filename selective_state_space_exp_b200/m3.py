@@ -549,21 +549,27 @@ def m3_mimo_down_gate(Y, w_down, z=None, *, out=None, stream=None):
 
 # ---- operators between the layer and a model's tokens ---------------------------
 # Their calls can be as short as a few microseconds on the device, so the
-# marshalling below keeps to plain integers, and shapes and workspace sizes are
-# looked up once per set of extents.
+# marshalling below keeps to plain integers and looks shapes and workspace sizes
+# up once per set of extents.
 
-def _enter(stream, device):
-    """The context a call is issued in (None: the current one will do) and its
-    stream handle.  Outputs and workspaces are made inside the context, so with
-    an explicit stream their memory belongs to that stream."""
+def _stream_on(stream, device):
+    """Handle of `stream`, or of the current stream of `device`."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return stream.cuda_stream
+
+
+def _elsewhere(stream, device):
+    """The context a call has to be made in, or None where the current one will
+    do.  Outputs and workspaces are made inside it, so with an explicit stream
+    their memory belongs to that stream."""
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        return torch.cuda.stream(stream), stream.cuda_stream
-    raw = torch._C._cuda_getCurrentRawStream(device.index)
+        return torch.cuda.stream(stream)
     if device.index == torch.cuda.current_device():
-        return None, raw
-    return torch.cuda.device(device), raw
+        return None
+    return torch.cuda.device(device)
 
 
 def _device_of(t):
@@ -576,33 +582,26 @@ def _addr(name, t, dtype, shape, device):
     """Address of t after checks of its type, shape, device and layout; None passes."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}: expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} is {tuple(t.shape)}: expected {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}: expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _scratch(nbytes, workspace, device):
+def _scratch(like, nbytes, workspace, device):
     """(address, bytes, the tensor to keep alive) of a call's workspace."""
     if workspace is None:
         if nbytes == 0:
             return None, 0, None
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = like.new_empty(nbytes, dtype=torch.uint8)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-
-
-def _run_in(ctx, fn):
-    if ctx is None:
-        return fn()
-    with ctx:
-        return fn()
 
 
 # ---- the grouped norm on the layer's output ------------------------------------
@@ -619,59 +618,80 @@ def _norm_plan(batch, seqlen, channels, groups, dtype, act, eps, backward, packe
     return ctypes.byref(shape), n.value
 
 
-def _norm_extent(x, groups, scope):
+def _norm_extent(shape, groups, scope):
     """(samples, positions of each) of x [..][C]."""
-    C = x.shape[-1] if x.dim() else 0
+    C = shape[-1] if shape else 0
     if groups < 1 or C < 1 or C % groups != 0:
-        raise ValueError(f"{tuple(x.shape)} channels last do not split into {groups} groups")
+        raise ValueError(f"{tuple(shape)} channels last do not split into {groups} groups")
     if scope == "token":
-        return x.numel() // C, 1
+        return shape.numel() // C, 1
     if scope == "sequence":
-        if x.dim() != 3:
+        if len(shape) != 3:
             raise ValueError("scope 'sequence' takes x [batch][seqlen][channels]")
-        return x.shape[0], x.shape[1]
+        return shape[0], shape[1]
     raise ValueError(f"scope is {scope!r}: expected 'token' or 'sequence'")
 
 
-def _norm_call(name, plan, packed, x, groups, stat, weight, bias, z, act, y, dy, mean, rstd,
-               workspace, stream, cu=None):
-    """Forward (dy None) or backward call; returns its outputs."""
-    backward = dy is not None
-    dev = _device_of(x)
-    C, f32, dt, shape = x.shape[-1], torch.float32, x.dtype, x.shape
+def _norm_forward(fn, plan, pre, x, stat, weight, bias, z, act, y, workspace, stream):
+    shape, dt, dev = x.shape, x.dtype, _device_of(x)
     if (z is not None) != (act == "gate"):
         raise ValueError("z belongs to act 'gate', and only to it")
-    px = _addr("x", x, dt, shape, dev)
-    pw, pb = _addr("weight", weight, f32, (C,), dev), _addr("bias", bias, f32, (C,), dev)
-    pz = _addr("z", z, dt, shape, dev)
-    ref, need = plan
-    pre = (_addr("cu_seqlens", cu, torch.int32, cu.shape, dev), shape[0]) if packed else ()
-    ctx, st = _enter(stream, dev)
+    args = (plan[0], *pre, _addr("x", x, dt, shape, dev),
+            _addr("weight", weight, torch.float32, shape[-1:], dev),
+            _addr("bias", bias, torch.float32, shape[-1:], dev), _addr("z", z, dt, shape, dev))
+    st, ctx = _stream_on(stream, dev), _elsewhere(stream, dev)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
+        if y is None:
+            y = torch.empty_like(x)
+            py = y.data_ptr()
+        else:
+            py = _addr("y", y, dt, shape, dev)
+        mean = x.new_empty(stat, dtype=torch.float32)
+        rstd = x.new_empty(stat, dtype=torch.float32)
+        pws, nws, keep = _scratch(x, plan[1], workspace, dev)
+        status = getattr(load(), fn)(*args, py, mean.data_ptr() or None, rstd.data_ptr() or None,
+                                     pws, nws, st)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+    if status:
+        raise M3Error(fn, status)
+    return y, mean, rstd
 
-    def forward_call():
-        out = torch.empty_like(x) if y is None else y
-        mu = torch.empty(stat, dtype=f32, device=dev)
-        inv = torch.empty(stat, dtype=f32, device=dev)
-        pws, nws, keep = _scratch(need, workspace, dev)
-        _check(name, getattr(load(), name)(
-            ref, *pre, px, pw, pb, pz, _addr("y", out, dt, shape, dev), mu.data_ptr() or None,
-            inv.data_ptr() or None, pws, nws, st))
-        return out, mu, inv
 
-    def backward_call():
-        pm, pr = _addr("mean", mean, f32, stat, dev), _addr("rstd", rstd, f32, stat, dev)
-        pdy = _addr("dy", dy, dt, shape, dev)
-        g = {"x": torch.empty_like(x), "weight": torch.empty((C,), dtype=f32, device=dev),
-             "bias": torch.empty((C,), dtype=f32, device=dev)}
+def _norm_backward(fn, plan, pre, x, stat, mean, rstd, dy, weight, bias, z, act, workspace,
+                   stream):
+    shape, dt, dev, f32 = x.shape, x.dtype, _device_of(x), torch.float32
+    if (z is not None) != (act == "gate"):
+        raise ValueError("z belongs to act 'gate', and only to it")
+    args = (plan[0], *pre, _addr("x", x, dt, shape, dev),
+            _addr("weight", weight, f32, shape[-1:], dev),
+            _addr("bias", bias, f32, shape[-1:], dev), _addr("z", z, dt, shape, dev),
+            _addr("mean", mean, f32, stat, dev), _addr("rstd", rstd, f32, stat, dev),
+            _addr("dy", dy, dt, shape, dev))
+    if dy is None or mean is None or rstd is None:
+        raise ValueError("the backward takes mean, rstd and dy")
+    st, ctx = _stream_on(stream, dev), _elsewhere(stream, dev)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
+        g = {"x": torch.empty_like(x), "weight": x.new_empty(shape[-1:], dtype=f32),
+             "bias": x.new_empty(shape[-1:], dtype=f32)}
+        pz = None
         if z is not None:
             g["z"] = torch.empty_like(x)
-        pws, nws, keep = _scratch(need, workspace, dev)
-        _check(name, getattr(load(), name)(
-            ref, *pre, px, pw, pb, pz, pm, pr, pdy, g["x"].data_ptr(), g["weight"].data_ptr(),
-            g["bias"].data_ptr(), g["z"].data_ptr() if z is not None else None, pws, nws, st))
-        return g
-
-    return _run_in(ctx, backward_call if backward else forward_call)
+            pz = g["z"].data_ptr()
+        pws, nws, keep = _scratch(x, plan[1], workspace, dev)
+        status = getattr(load(), fn)(*args, g["x"].data_ptr() or None, g["weight"].data_ptr(),
+                                     g["bias"].data_ptr(), pz, pws, nws, st)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+    if status:
+        raise M3Error(fn, status)
+    return g
 
 
 def m3_group_norm_fwd(x, groups: int, weight=None, bias=None, z=None, *, act="none",
@@ -681,40 +701,37 @@ def m3_group_norm_fwd(x, groups: int, weight=None, bias=None, z=None, *, act="no
     over all positions of a sequence too (scope "sequence", x [b][L][C]).
     act "none", "silu", or "gate" (times silu(z), z like x); weight, bias [C]
     fp32 or None.  Returns (y, mean, rstd), the statistics [samples][groups]."""
-    batch, seqlen = _norm_extent(x, groups, scope)
-    stat = (batch, groups)
-    if batch == 0:  # no sample: to the library, one without positions
-        batch, seqlen = 1, 0
-    plan = _norm_plan(batch, seqlen, x.shape[-1], groups, x.dtype, act, eps, False, False)
-    return _norm_call("m3_group_norm_fwd", plan, False, x, groups, stat, weight, bias, z, act, y,
-                      None, None, None, workspace, stream)
+    batch, seqlen = _norm_extent(x.shape, groups, scope)
+    # no sample: to the library, one without positions
+    plan = _norm_plan(batch or 1, seqlen if batch else 0, x.shape[-1], groups, x.dtype, act, eps,
+                      False, False)
+    return _norm_forward("m3_group_norm_fwd", plan, (), x, (batch, groups), weight, bias, z, act,
+                         y, workspace, stream)
 
 
 def m3_group_norm_bwd(x, groups: int, mean, rstd, dy, weight=None, bias=None, z=None, *,
                       act="none", scope="token", workspace=None, stream=None):
     """Backward of m3_group_norm_fwd from its inputs and statistics: a dict of
     x and (act "gate") z in the io dtype, weight and bias fp32 [C]."""
-    batch, seqlen = _norm_extent(x, groups, scope)
-    stat = (batch, groups)
-    if batch == 0:  # no sample: to the library, one without positions
-        batch, seqlen = 1, 0
-    plan = _norm_plan(batch, seqlen, x.shape[-1], groups, x.dtype, act, 0.0, True, False)
-    return _norm_call("m3_group_norm_bwd", plan, False, x, groups, stat, weight, bias, z, act,
-                      None, dy, mean, rstd, workspace, stream)
+    batch, seqlen = _norm_extent(x.shape, groups, scope)
+    plan = _norm_plan(batch or 1, seqlen if batch else 0, x.shape[-1], groups, x.dtype, act, 0.0,
+                      True, False)
+    return _norm_backward("m3_group_norm_bwd", plan, (), x, (batch, groups), mean, rstd, dy,
+                          weight, bias, z, act, workspace, stream)
 
 
 def _norm_packed(cu_seqlens, x, groups, max_seqlen):
-    if cu_seqlens.dtype != torch.int32:
-        raise TypeError("cu_seqlens must be int32")
+    """(sequences, longest, the call's extra arguments) of a packed batch."""
     if x.dim() != 2:
         raise ValueError("a packed batch is x [tokens][channels]")
-    _norm_extent(x, groups, "token")
+    _norm_extent(x.shape, groups, "token")
     S = cu_seqlens.numel() - 1
     if cu_seqlens.dim() != 1 or S < 1:
         raise ValueError("cu_seqlens holds no sequence")
+    cu = _addr("cu_seqlens", cu_seqlens, torch.int32, cu_seqlens.shape, _device_of(x))
     if max_seqlen is None:
         max_seqlen = int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item())
-    return S, max_seqlen
+    return S, max_seqlen, (cu, x.shape[0])
 
 
 def m3_group_norm_fwd_varlen(cu_seqlens, x, groups: int, weight=None, bias=None, z=None, *,
@@ -723,60 +740,69 @@ def m3_group_norm_fwd_varlen(cu_seqlens, x, groups: int, weight=None, bias=None,
     """m3_group_norm_fwd over the sequences of a packed batch: x [T][C],
     cu_seqlens [S+1] int32 on the device; max_seqlen as m3_scan_fwd_varlen.
     Rows of y outside every sequence are left as they are."""
-    S, L = _norm_packed(cu_seqlens, x, groups, max_seqlen)
+    S, L, pre = _norm_packed(cu_seqlens, x, groups, max_seqlen)
     plan = _norm_plan(S, L, x.shape[1], groups, x.dtype, act, eps, False, True)
-    return _norm_call("m3_group_norm_fwd_varlen", plan, True, x, groups, (S, groups), weight,
-                      bias, z, act, y, None, None, None, workspace, stream, cu_seqlens)
+    return _norm_forward("m3_group_norm_fwd_varlen", plan, pre, x, (S, groups), weight, bias, z,
+                         act, y, workspace, stream)
 
 
 def m3_group_norm_bwd_varlen(cu_seqlens, x, groups: int, mean, rstd, dy, weight=None, bias=None,
                              z=None, *, act="none", max_seqlen=None, workspace=None, stream=None):
     """Backward of m3_group_norm_fwd_varlen (the dict of m3_group_norm_bwd);
     rows of dx and dz outside every sequence are undefined."""
-    S, L = _norm_packed(cu_seqlens, x, groups, max_seqlen)
+    S, L, pre = _norm_packed(cu_seqlens, x, groups, max_seqlen)
     plan = _norm_plan(S, L, x.shape[1], groups, x.dtype, act, 0.0, True, True)
-    return _norm_call("m3_group_norm_bwd_varlen", plan, True, x, groups, (S, groups), weight,
-                      bias, z, act, None, dy, mean, rstd, workspace, stream, cu_seqlens)
+    return _norm_backward("m3_group_norm_bwd_varlen", plan, pre, x, (S, groups), mean, rstd, dy,
+                          weight, bias, z, act, workspace, stream)
 
 
 # ---- the head's cross entropy ---------------------------------------------------
 
+@functools.lru_cache(maxsize=4096)
+def _xent_bytes(tokens, vocab, width):
+    """Workspace bytes of the forward and of the backward."""
+    n, m = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    L = load()
+    _check("m3_linear_xent_fwd_workspace_size",
+           L.m3_linear_xent_fwd_workspace_size(tokens, vocab, width, ctypes.byref(n)))
+    _check("m3_linear_xent_bwd_workspace_size",
+           L.m3_linear_xent_bwd_workspace_size(tokens, vocab, width, ctypes.byref(m)))
+    return n.value, m.value
+
+
 def _xent_args(h, W, targets):
-    """(tokens, vocabulary, width, device) and the addresses of the three."""
-    bf16 = torch.bfloat16
+    """(tokens, vocabulary, width, addresses of the three)."""
     if W.dim() != 2 or h.dim() < 1 or h.shape[-1] != W.shape[1]:
         raise ValueError(f"h is {tuple(h.shape)} and W {tuple(W.shape)}: expected [..][K], [V][K]")
     dev = _device_of(h)
     V, K = W.shape
-    ptrs = (_addr("h", h, bf16, h.shape, dev), _addr("W", W, bf16, W.shape, dev),
+    return (targets.numel(), V, K, _addr("h", h, torch.bfloat16, h.shape, dev),
+            _addr("W", W, torch.bfloat16, W.shape, dev),
             _addr("targets", targets, torch.int64, h.shape[:-1], dev))
-    return (targets.numel(), V, K), dev, ptrs
-
-
-@functools.lru_cache(maxsize=4096)
-def _xent_bytes(name, sizes):
-    n = ctypes.c_size_t(0)
-    _check(name, getattr(load(), name)(*sizes, ctypes.byref(n)))
-    return n.value
 
 
 def m3_linear_xent_fwd(h, W, targets, *, ignore_index: int = -100, workspace=None, stream=None):
     """Softmax cross entropy of logits = h W^T, which are never stored: h [..][K]
     bf16, W [V][K] bf16, targets [..] int64 (ignore_index: not scored).  Returns
     (loss, lse), fp32 and shaped like targets."""
-    sizes, dev, ptrs = _xent_args(h, W, targets)
-    need = _xent_bytes("m3_linear_xent_fwd_workspace_size", sizes)
-    ctx, st = _enter(stream, dev)
-
-    def call():
-        loss = torch.empty(targets.shape, dtype=torch.float32, device=dev)
-        lse = torch.empty(targets.shape, dtype=torch.float32, device=dev)
-        pws, nws, keep = _scratch(need, workspace, dev)
-        _check("m3_linear_xent_fwd", load().m3_linear_xent_fwd(
-            *sizes, *ptrs, ignore_index, loss.data_ptr(), lse.data_ptr(), pws, nws, st))
-        return loss, lse
-
-    return _run_in(ctx, call)
+    args = _xent_args(h, W, targets)
+    dev = h.device
+    need = _xent_bytes(*args[:3])[0]
+    st, ctx = _stream_on(stream, dev), _elsewhere(stream, dev)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
+        loss = torch.empty_like(targets, dtype=torch.float32)
+        lse = torch.empty_like(targets, dtype=torch.float32)
+        pws, nws, keep = _scratch(h, need, workspace, dev)
+        status = load().m3_linear_xent_fwd(*args, ignore_index, loss.data_ptr(), lse.data_ptr(),
+                                           pws, nws, st)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+    if status:
+        raise M3Error("m3_linear_xent_fwd", status)
+    return loss, lse
 
 
 def m3_linear_xent_bwd(h, W, targets, lse, dloss, *, ignore_index: int = -100, want_dh=True,
@@ -784,22 +810,27 @@ def m3_linear_xent_bwd(h, W, targets, lse, dloss, *, ignore_index: int = -100, w
     """Backward of m3_linear_xent_fwd: (dh, dW) bf16, the gradients of
     sum(loss * dloss) (None for one that is not wanted).  lse as the forward
     gave it, dloss fp32 shaped like targets."""
-    sizes, dev, ptrs = _xent_args(h, W, targets)
+    args = _xent_args(h, W, targets)
+    dev = h.device
     plse = _addr("lse", lse, torch.float32, targets.shape, dev)
     pdl = _addr("dloss", dloss, torch.float32, targets.shape, dev)
-    need = _xent_bytes("m3_linear_xent_bwd_workspace_size", sizes)
-    ctx, st = _enter(stream, dev)
-
-    def call():
+    need = _xent_bytes(*args[:3])[1]
+    st, ctx = _stream_on(stream, dev), _elsewhere(stream, dev)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
         dh = torch.empty_like(h) if want_dh else None
         dW = torch.empty_like(W) if want_dW else None
-        pws, nws, keep = _scratch(need, workspace, dev)
-        _check("m3_linear_xent_bwd", load().m3_linear_xent_bwd(
-            *sizes, *ptrs, ignore_index, plse, pdl, dh.data_ptr() if want_dh else None,
-            dW.data_ptr() if want_dW else None, pws, nws, st))
-        return dh, dW
-
-    return _run_in(ctx, call)
+        pws, nws, keep = _scratch(h, need, workspace, dev)
+        status = load().m3_linear_xent_bwd(*args, ignore_index, plse, pdl,
+                                           dh.data_ptr() if want_dh else None,
+                                           dW.data_ptr() if want_dW else None, pws, nws, st)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+    if status:
+        raise M3Error("m3_linear_xent_bwd", status)
+    return dh, dW
 
 
 # ---- 4-bit weights ---------------------------------------------------------------
@@ -815,18 +846,21 @@ def m3_w4_quantize(W, group: int = 128, *, symmetric=False, stream=None):
         raise ValueError(f"{K} inputs do not split into groups of {group} (32, 64 or 128)")
     dev = _device_of(W)
     code, pW = _io_code(W.dtype), _addr("W", W, W.dtype, W.shape, dev)
-    ctx, st = _enter(stream, dev)
-
-    def call():
-        codes = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
-        scales = torch.empty((N, K // group), dtype=torch.bfloat16, device=dev)
-        zeros = None if symmetric else torch.empty((N, K // group), dtype=torch.uint8, device=dev)
-        _check("m3_w4_quantize", load().m3_w4_quantize(
-            N, K, group, code, pW, codes.data_ptr(), scales.data_ptr(),
-            None if symmetric else zeros.data_ptr(), st))
-        return codes, scales, zeros
-
-    return _run_in(ctx, call)
+    st, ctx = _stream_on(stream, dev), _elsewhere(stream, dev)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
+        codes = W.new_empty((N, K // 2), dtype=torch.uint8)
+        scales = W.new_empty((N, K // group), dtype=torch.bfloat16)
+        zeros = None if symmetric else W.new_empty((N, K // group), dtype=torch.uint8)
+        status = load().m3_w4_quantize(N, K, group, code, pW, codes.data_ptr(), scales.data_ptr(),
+                                       None if symmetric else zeros.data_ptr(), st)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+    if status:
+        raise M3Error("m3_w4_quantize", status)
+    return codes, scales, zeros
 
 
 def m3_linear_w4(A, codes, scales, zeros=None, bias=None, *, out=None, out_dtype=torch.bfloat16,
@@ -837,27 +871,37 @@ def m3_linear_w4(A, codes, scales, zeros=None, bias=None, *, out=None, out_dtype
     fp32)."""
     if codes.dim() != 2 or scales.dim() != 2:
         raise ValueError("codes and scales are [N][..]")
-    N, K = codes.shape[0], 2 * codes.shape[1]
-    if A.dim() < 1 or A.shape[-1] != K:
-        raise ValueError(f"A is {tuple(A.shape)}: expected [..][{K}]")
-    ng = scales.shape[1]
+    N, half = codes.shape
+    K, ng = 2 * half, scales.shape[1]
+    shape = A.shape
+    if not shape or shape[-1] != K:
+        raise ValueError(f"A is {tuple(shape)}: expected [..][{K}]")
     if ng == 0 or K % ng != 0:
         raise ValueError(f"scales is {tuple(scales.shape)} for {K} inputs")
-    dev, bf16, u8 = _device_of(A), torch.bfloat16, torch.uint8
+    dev = _device_of(A)
     if out is not None:
         out_dtype = out.dtype
+    groups = (N, ng)
+    args = (shape.numel() // K, N, K, K // ng, _addr("A", A, torch.bfloat16, shape, dev),
+            _addr("codes", codes, torch.uint8, (N, half), dev),
+            _addr("scales", scales, torch.bfloat16, groups, dev),
+            _addr("zeros", zeros, torch.uint8, groups, dev),
+            _addr("bias", bias, torch.float32, (N,), dev))
     code = _io_code(out_dtype)
-    pA, pc = _addr("A", A, bf16, A.shape, dev), _addr("codes", codes, u8, codes.shape, dev)
-    ps = _addr("scales", scales, bf16, (N, ng), dev)
-    pz, pb = _addr("zeros", zeros, u8, (N, ng), dev), _addr("bias", bias, torch.float32, (N,), dev)
-    full = A.shape[:-1] + (N,)
-    ctx, st = _enter(stream, dev)
-
-    def call():
-        o = torch.empty(full, dtype=out_dtype, device=dev) if out is None else out
-        _check("m3_linear_w4", load().m3_linear_w4(
-            A.numel() // K, N, K, K // ng, pA, pc, ps, pz, pb, _addr("out", o, out_dtype, full, dev),
-            code, st))
-        return o
-
-    return _run_in(ctx, call)
+    st, ctx = _stream_on(stream, dev), _elsewhere(stream, dev)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
+        full = shape[:-1] + (N,)
+        if out is None:
+            out = A.new_empty(full, dtype=out_dtype)
+            po = out.data_ptr()
+        else:
+            po = _addr("out", out, out_dtype, full, dev)
+        status = load().m3_linear_w4(*args, po, code, st)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+    if status:
+        raise M3Error("m3_linear_w4", status)
+    return out
