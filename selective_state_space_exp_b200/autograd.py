@@ -105,3 +105,95 @@ def m3_scan_varlen(cu_seqlens, x, dt, A, lam, theta, B, C, chunk: int = 64, h0=N
         max_seqlen = int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item()) if S > 0 else 0
     return M3ScanVarlen.apply(chunk, max_seqlen, cu_seqlens, x, dt, A, lam, theta, B, C, h0,
                               B_prev, x_prev)
+
+
+# ---- operators between the layer and a model's tokens ---------------------------
+
+class M3GroupNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, cu_seqlens, max_seqlen, groups, act, eps, scope, x, weight, bias, z):
+        kw = dict(weight=weight, bias=bias, z=z, act=act, eps=eps)
+        if cu_seqlens is None:
+            y, mean, rstd = m3.m3_group_norm_fwd(x, groups, scope=scope, **kw)
+        else:
+            # rows outside every sequence are not written by the call
+            y, mean, rstd = m3.m3_group_norm_fwd_varlen(cu_seqlens, x, groups, y=x.clone(),
+                                                        max_seqlen=max_seqlen, **kw)
+        ctx.groups, ctx.act, ctx.scope, ctx.max_seqlen = groups, act, scope, max_seqlen
+        ctx.save_for_backward(cu_seqlens, x, weight, bias, z, mean, rstd)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        cu, x, weight, bias, z, mean, rstd = ctx.saved_tensors
+        dy = dy.to(x.dtype).contiguous()
+        kw = dict(weight=weight, bias=bias, z=z, act=ctx.act)
+        if cu is None:
+            g = m3.m3_group_norm_bwd(x, ctx.groups, mean, rstd, dy, scope=ctx.scope, **kw)
+        else:
+            g = m3.m3_group_norm_bwd_varlen(cu, x, ctx.groups, mean, rstd, dy,
+                                            max_seqlen=ctx.max_seqlen, **kw)
+            # the gradients of rows outside every sequence: y there is x itself
+            outside = _outside(cu, x.shape[0])
+            g["x"] = torch.where(outside, dy, g["x"])
+            if z is not None:
+                g["z"] = torch.where(outside, torch.zeros_like(z), g["z"])
+        need = ctx.needs_input_grad[6:]
+        return (None,) * 6 + tuple(g.get(name) if want else None for name, want in
+                                   zip(("x", "weight", "bias", "z"), need))
+
+
+def _outside(cu_seqlens, total):
+    """[total][1] bool: rows that belong to no sequence (before the first, behind the last)."""
+    row = torch.arange(total, device=cu_seqlens.device)
+    return ((row < cu_seqlens[0]) | (row >= cu_seqlens[-1]))[:, None]
+
+
+def group_norm(x, groups: int, weight=None, bias=None, z=None, *, act="none", eps: float = 1e-5,
+               scope="token"):
+    """Differentiable m3.m3_group_norm_fwd: y alone, gradients of x, weight, bias
+    and z by m3_group_norm_bwd (weight and bias fp32)."""
+    return M3GroupNorm.apply(None, None, groups, act, eps, scope, x, weight, bias, z)
+
+
+def group_norm_varlen(cu_seqlens, x, groups: int, weight=None, bias=None, z=None, *, act="none",
+                      eps: float = 1e-5, max_seqlen=None):
+    """group_norm over the sequences of a packed batch (x [T][C]); rows outside
+    every sequence pass through unchanged."""
+    if max_seqlen is None:
+        max_seqlen = int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item())
+    return M3GroupNorm.apply(cu_seqlens, max_seqlen, groups, act, eps, "sequence", x, weight,
+                             bias, z)
+
+
+class M3LinearXent(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ignore_index, targets, h, W):
+        loss, lse = m3.m3_linear_xent_fwd(h, W, targets, ignore_index=ignore_index)
+        ctx.ignore_index = ignore_index
+        ctx.save_for_backward(targets, h, W, lse)
+        return loss
+
+    @staticmethod
+    def backward(ctx, dloss):
+        targets, h, W, lse = ctx.saved_tensors
+        dh, dW = m3.m3_linear_xent_bwd(h, W, targets, lse, dloss.contiguous(),
+                                       ignore_index=ctx.ignore_index,
+                                       want_dh=ctx.needs_input_grad[2],
+                                       want_dW=ctx.needs_input_grad[3])
+        return None, None, dh, dW
+
+
+def linear_cross_entropy(h, W, targets, *, ignore_index: int = -100, reduction="mean"):
+    """Softmax cross entropy of the head W [V][K] on hidden states h [..][K]
+    (bf16) without the logits, by m3_linear_xent_fwd / _bwd.  reduction "none"
+    (shaped like targets), "sum", or "mean" over the scored tokens (0 where there
+    is none).  Gradients of h and W, in bf16."""
+    if reduction not in ("none", "sum", "mean"):
+        raise ValueError(f"reduction is {reduction!r}: expected 'none', 'sum' or 'mean'")
+    loss = M3LinearXent.apply(ignore_index, targets, h, W)
+    if reduction == "none":
+        return loss
+    if reduction == "sum":
+        return loss.sum()
+    return loss.sum() / (targets != ignore_index).sum().clamp(min=1)

@@ -108,8 +108,9 @@ int norm_call(const m3_norm_shape* s, const int32_t* cu, int64_t tokens, bool va
                       {backward ? nullptr : io.mean, ns}, {backward ? nullptr : io.rstd, ns},
                       {ws, ws_bytes}};
   for (const Span& o : out) {
+    const bool is_y = io.y && o.p == io.y;  // may be x or z itself
     for (const Span& i : in)
-      if (overlap(o, i) && !(o.p == io.y && io.y && (i.p == io.x || i.p == io.z)))
+      if (overlap(o, i) && !(is_y && i.p == o.p && (i.p == io.x || i.p == io.z)))
         return M3_ERR_INVALID_ARGUMENT;
     for (const Span& q : out)
       if (&o != &q && overlap(o, q)) return M3_ERR_INVALID_ARGUMENT;
