@@ -41,27 +41,36 @@ namespace {
 
 using namespace tc;
 
-constexpr int kBM = 128, kBN = 256, kBK = 64;
-constexpr int kStages = 4;
+constexpr int kBM = 128, kBN = 256, kBK = 64;  // a CTA's rows of a tile, columns, reduction step
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2;
-constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kBlk = 64 * kBK * 2;  // an MN-major block: 64 columns x 64 reduction rows
-constexpr int kBarOff = kStages * kStageBytes;
-constexpr int kSmem = kBarOff + (2 * kStages + 5) * 8 + 16;
 constexpr int kTmemCols = 2 * kBN;
-constexpr int kGroupM = 16;  // row tiles that share a column tile while it is in L2
+
+// CG: CTAs that share a tile of CG * 128 rows (a pair's tensor cores work on one
+// tile, each CTA holding its own rows of A and half the columns of B, which
+// halves what the pair reads of B).
+template <int CG>
+struct Cfg {
+  static constexpr int A_BYTES = kBM * kBK * 2;
+  static constexpr int B_COLS = kBN / CG;
+  static constexpr int STAGE = A_BYTES + B_COLS * kBK * 2;
+  static constexpr int STAGES = CG == 2 ? 6 : 4;
+  static constexpr int BAR_OFF = STAGES * STAGE;
+  static constexpr int SMEM = BAR_OFF + (2 * STAGES + 5) * 8 + 16;
+  static_assert(SMEM + 1024 <= 232448, "shared memory");
+};
+
+constexpr int kGroupRows = 2048;  // rows that share a column tile while it is in L2
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-static_assert(kSmem + 1024 <= 232448, "shared memory");
 
 enum Mode { kStats = 0, kDlogits = 1, kGrad = 2 };
 
 struct GemmArgs {
   int64_t M, N;           // extent of the output
   int kb, kb_per;         // reduction blocks in all, and of one split
-  int mt, nt, splits;     // tiles
+  int cg, mt, nt, splits; // CTAs of a tile; tiles
   int* status;
   // stats, dlogits: rows are tokens, columns classes v0 + n
   const int64_t* targets;
@@ -113,14 +122,83 @@ __device__ __forceinline__ void tma_2d(void* dst, const void* map, int c0, int c
       : "memory");
 }
 
+// Pair forms (CTA group 2): both CTAs' loads complete on the first one's barrier,
+// whose thread issues the MMAs of both; a commit reaches the barriers of both.
+__device__ __forceinline__ uint32_t in_first_cta(const void* p) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+__device__ __forceinline__ void tma_2d_pair(void* dst, const void* map, int c0, int c1,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (CG == 1) {
+    mma_bf16_ss(d, a, b, idesc, acc);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc));
+  }
+}
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (CG == 1) {
+    mma_commit(bar);
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void alloc(uint32_t* holder) {
+  if constexpr (CG == 1) {
+    tmem_alloc(holder, kTmemCols);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(holder)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void dealloc(uint32_t taddr) {
+  if constexpr (CG == 1)
+    tmem_dealloc(taddr, kTmemCols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(kTmemCols)
+                 : "memory");
+}
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+
 struct Tile {
   int m, n, split;
 };
 
-// Tiles of one split first; inside it bands of kGroupM row tiles, down each
-// column of a band before the next column: the CTAs running at one time share
-// a few row and column tiles, which stay in L2.
+// Tiles of one split first; inside it bands of kGroupRows rows, down each column
+// of a band before the next column: the CTAs running at one time share a few row
+// and column tiles, which stay in L2.
+template <int CG>
 __device__ __forceinline__ Tile tile_of(const GemmArgs& g, int64_t t) {
+  constexpr int kGroupM = kGroupRows / (CG * kBM);
   const int64_t per = (int64_t)g.mt * g.nt;
   Tile o;
   o.split = (int)(t / per);
@@ -134,15 +212,20 @@ __device__ __forceinline__ Tile tile_of(const GemmArgs& g, int64_t t) {
 }
 
 // Operand tiles of one stage: K-major [rows][64] as one box; MN-major as blocks
-// of 64 columns, each 64 reduction rows of 128 bytes.
-template <bool MN, int ROWS>
+// of 64 columns, each 64 reduction rows of 128 bytes.  bar: a shared::cluster
+// address.
+template <int CG, bool MN, int ROWS>
 __device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, int row0, int k0,
-                                             uint64_t* bar) {
+                                             uint64_t* own, uint32_t bar) {
+  auto load = [&](uint8_t* d, int c0, int c1) {
+    if constexpr (CG == 1) tma_2d(d, map, c0, c1, own);
+    else tma_2d_pair(d, map, c0, c1, bar);
+  };
   if constexpr (MN) {
 #pragma unroll
-    for (int i = 0; i < ROWS / 64; ++i) tma_2d(dst + i * kBlk, map, row0 + i * 64, k0, bar);
+    for (int i = 0; i < ROWS / 64; ++i) load(dst + i * kBlk, row0 + i * 64, k0);
   } else {
-    tma_2d(dst, map, k0, row0, bar);
+    load(dst, k0, row0);
   }
 }
 
@@ -166,9 +249,9 @@ __device__ __forceinline__ float largest_dloss(const GemmArgs& g, float* s_max) 
 }
 
 template <int MODE>
-__device__ __forceinline__ void epilogue(const GemmArgs& g, const Tile& t, uint32_t tcol, int q,
-                                         int half, int lane, float unit) {
-  const int64_t m = (int64_t)t.m * kBM + 32 * q + lane;
+__device__ __forceinline__ void epilogue(const GemmArgs& g, const Tile& t, int64_t row0,
+                                         uint32_t tcol, int q, int half, int lane, float unit) {
+  const int64_t m = row0 + 32 * q + lane;
   const int64_t n0 = (int64_t)t.n * kBN + half * (kBN / 2);
   const bool on = m < g.M;
   if constexpr (MODE == kStats) {
@@ -276,9 +359,11 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const Tile& t, uint3
   }
 }
 
-template <int MODE, bool AMN, bool BMN>
+template <int CG, int MODE, bool AMN, bool BMN>
 __global__ void __launch_bounds__(kThreads, 1)
 xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
+  using C = Cfg<CG>;
+  constexpr int kStages = C::STAGES;
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sbase = smem_u32(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -286,13 +371,15 @@ xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
     if (tid == 0 && g.status) atomicCAS(g.status, 0, (int)M3_ERR_CUDA);
     return;
   }
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kBarOff);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* s_fin = acc_empty + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_fin + 1);
   const int64_t tiles = (int64_t)g.mt * g.nt * g.splits;
+  const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0;  // a pair is two neighbouring blocks
+  const int64_t first = blockIdx.x / CG, step = gridDim.x / CG;
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -301,15 +388,16 @@ xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 32 * kEpiWarps);
+      mbar_init(&acc_empty[b], CG * kEpiWarps);
     }
     mbar_init(s_fin, 1);
     fence_mbar_init();
   }
-  if (warp == 1) {
-    tmem_alloc(s_tmem, kTmemCols);
-    tmem_relinquish();
+  if (CG == 2) {
+    __syncthreads();
+    pair_sync();  // the other CTA's barriers are ready
   }
+  if (warp == 1) alloc<CG>(s_tmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -318,28 +406,32 @@ xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
   if (warp == 0 && lane == 0) {
     uint32_t it = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile tl = tile_of(g, t);
+    for (int64_t t = first; t < tiles && ok; t += step) {
+      const Tile tl = tile_of<CG>(g, t);
       const int k0 = tl.split * g.kb_per, k1 = k0 + g.kb_per < g.kb ? k0 + g.kb_per : g.kb;
       for (int kb = k0; kb < k1; ++kb, ++it) {
         const int s = (int)(it % kStages);
         if (!wait(&empty[s], ((it / kStages) & 1u) ^ 1u, g.status)) { ok = false; break; }
-        uint8_t* st = sm + s * kStageBytes;
-        mbar_expect_tx(&full[s], (uint32_t)kStageBytes);
-        load_operand<AMN, kBM>(st, &maps.a, tl.m * kBM, kb * kBK, &full[s]);
-        load_operand<BMN, kBN>(st + kABytes, &maps.b, tl.n * kBN, kb * kBK, &full[s]);
+        uint8_t* st = sm + s * C::STAGE;
+        const uint32_t bar = CG == 2 ? in_first_cta(&full[s]) : 0;
+        if (rank == 0) mbar_expect_tx(&full[s], (uint32_t)(CG * C::STAGE));
+        load_operand<CG, AMN, kBM>(st, &maps.a, (tl.m * CG + rank) * kBM, kb * kBK, &full[s], bar);
+        load_operand<CG, BMN, C::B_COLS>(st + C::A_BYTES, &maps.b, tl.n * kBN + rank * C::B_COLS,
+                                         kb * kBK, &full[s], bar);
       }
     }
-    // let the last stages' copies land (bounded) before the CTA can exit
+    // let the last stages' copies land (bounded) before the CTA can exit: the
+    // first CTA's barriers see both CTAs' copies, the other CTA waits for the
+    // MMAs that have read its own
     for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-      wait(&full[j % kStages], (j / kStages) & 1u, g.status);
-  } else if (warp == 1 && lane == 0) {
-    const uint32_t idesc = idesc_bf16(kBM, kBN, AMN, BMN);
+      wait(rank == 0 ? &full[j % kStages] : &empty[j % kStages], (j / kStages) & 1u, g.status);
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    const uint32_t idesc = idesc_bf16(CG * kBM, kBN, AMN, BMN);
     uint32_t it = 0;
     int j = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++j) {
-      const Tile tl = tile_of(g, t);
+    for (int64_t t = first; t < tiles && ok; t += step, ++j) {
+      const Tile tl = tile_of<CG>(g, t);
       const int k0 = tl.split * g.kb_per, k1 = k0 + g.kb_per < g.kb ? k0 + g.kb_per : g.kb;
       const int b = j & 1;
       if (!wait(&acc_empty[b], ((j >> 1) & 1) ^ 1u, g.status)) break;
@@ -349,17 +441,17 @@ xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
         const int s = (int)(it % kStages);
         if (!wait(&full[s], (it / kStages) & 1u, g.status)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t st = sbase + (uint32_t)(s * kStageBytes);
+        const uint32_t st = sbase + (uint32_t)(s * C::STAGE);
         // K-major: 16 reduction columns are 32 bytes on; MN-major: 16 rows of 128 bytes
         const uint64_t ad = sw128_desc(st, AMN ? kBlk : 16, 1024);
-        const uint64_t bd = sw128_desc(st + kABytes, BMN ? kBlk : 16, 1024);
+        const uint64_t bd = sw128_desc(st + C::A_BYTES, BMN ? kBlk : 16, 1024);
 #pragma unroll
         for (int k4 = 0; k4 < kBK / 16; ++k4)
-          mma_bf16_ss(dcol, ad + (uint64_t)(k4 * (AMN ? 128 : 2)),
-                      bd + (uint64_t)(k4 * (BMN ? 128 : 2)), idesc, kb > k0 || k4 > 0);
-        mma_commit(&empty[s]);
+          mma<CG>(dcol, ad + (uint64_t)(k4 * (AMN ? 128 : 2)),
+                  bd + (uint64_t)(k4 * (BMN ? 128 : 2)), idesc, kb > k0 || k4 > 0);
+        commit<CG>(&empty[s]);
       }
-      if (ok) mma_commit(&acc_full[b]);
+      if (ok) commit<CG>(&acc_full[b]);
     }
   } else if (warp >= 2) {
     const int q = warp & 3;  // TMEM lane quadrant this warp may access
@@ -372,15 +464,20 @@ xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
     }
     if constexpr (MODE == kGrad) unit = *g.unit;
     int j = 0;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++j) {
+    for (int64_t t = first; t < tiles; t += step, ++j) {
       const int b = j & 1;
-      if (!wait(&acc_full[b], (j >> 1) & 1u, g.status)) break;
+      if (!__all_sync(0xffffffffu, wait(&acc_full[b], (j >> 1) & 1u, g.status))) break;
       tc_fence_after();
-      epilogue<MODE>(g, tile_of(g, t),
+      const Tile tl = tile_of<CG>(g, t);
+      epilogue<MODE>(g, tl, (int64_t)(tl.m * CG + rank) * kBM,
                      tm + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * kBN + half * (kBN / 2)), q,
                      half, lane, unit);
       tc_fence_before();
-      arrive(&acc_empty[b]);
+      __syncwarp();
+      if (lane == 0) {  // the MMA thread's CTA learns it from both
+        if constexpr (CG == 1) arrive(&acc_empty[b]);
+        else arrive_at(in_first_cta(&acc_empty[b]));
+      }
     }
   }
 
@@ -388,14 +485,13 @@ xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) {
-    if (lane == 0) {
-      mma_commit(s_fin);
-      wait(s_fin, 0, g.status);
-    }
-    __syncwarp();
-    tmem_dealloc(tm, kTmemCols);
+  if (warp == 1 && lane == 0 && rank == 0) {
+    commit<CG>(s_fin);
+    wait(s_fin, 0, g.status);
   }
+  __syncwarp();
+  if (CG == 2) pair_sync();
+  if (warp == 1) dealloc<CG>(tm);
 }
 
 // (maximum, sum) of the exponentials of two sets.
@@ -499,23 +595,41 @@ struct Operand {
   int64_t rows, cols, ld;
 };
 
-template <int MODE, bool AMN, bool BMN>
-cudaError_t gemm(const GemmArgs& g, const Operand& a, const Operand& b, cudaStream_t s) {
+template <int CG, int MODE, bool AMN, bool BMN>
+cudaError_t gemm_cg(const GemmArgs& g, const Operand& a, const Operand& b, cudaStream_t s) {
+  using C = Cfg<CG>;
   Maps maps;
   memset(&maps, 0, sizeof(maps));
   if (!encode(&maps.a, a.p, a.rows, a.cols, a.ld, AMN ? kBK : kBM) ||
-      !encode(&maps.b, b.p, b.rows, b.cols, b.ld, BMN ? kBK : kBN))
+      !encode(&maps.b, b.p, b.rows, b.cols, b.ld, BMN ? kBK : C::B_COLS))
     return cudaErrorInvalidValue;
-  auto kern = xent_gemm_kernel<MODE, AMN, BMN>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  auto kern = xent_gemm_kernel<CG, MODE, AMN, BMN>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
   e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)g.mt * g.nt * g.splits;
-  kern<<<(unsigned)(tiles < sms ? tiles : sms), kThreads, kSmem, s>>>(g, maps);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)(CG * (tiles < sms / CG ? tiles : sms / CG)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = CG;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = CG > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, g, maps);
+}
+
+template <int MODE, bool AMN, bool BMN>
+cudaError_t gemm(const GemmArgs& g, const Operand& a, const Operand& b, cudaStream_t s) {
+  return g.cg == 2 ? gemm_cg<2, MODE, AMN, BMN>(g, a, b, s) : gemm_cg<1, MODE, AMN, BMN>(g, a, b, s);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -523,7 +637,10 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 void set_tiles(GemmArgs* g, int64_t M, int64_t N, int64_t K, int splits) {
   g->M = M;
   g->N = N;
-  g->mt = (int)ceil_div(M, kBM);
+  // pairs of CTAs where their larger tiles still fill most SMs
+  const int64_t pairs = ceil_div(M, 2 * kBM) * ceil_div(N, kBN);
+  g->cg = splits == 1 && pairs >= kPlanSms / 2 * 3 / 4 ? 2 : 1;
+  g->mt = (int)ceil_div(M, g->cg * kBM);
   g->nt = (int)ceil_div(N, kBN);
   g->kb = (int)ceil_div(K, kBK);
   g->kb_per = (int)ceil_div(g->kb, splits);
