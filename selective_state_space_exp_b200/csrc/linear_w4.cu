@@ -57,9 +57,9 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a
 }
 
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // (v & mask) | magic as one instruction.
@@ -263,21 +263,54 @@ __device__ __forceinline__ void box_products(const uint8_t* codes, const uint8_t
 template <int G, int NT>
 __device__ __forceinline__ void stage_tokens(const W4Args& a, uint8_t* xs, int64_t m0,
                                              int64_t box0, int boxes) {
-  const int n = 2 * boxes;
-  for (int i = threadIdx.x; i < NT * n * 128; i += kThreads) {
-    const int lane = i & 31, w = (i >> 5) & 3;
-    const int ch = (i >> 7) % n, t = (i >> 7) / n;
-    const int64_t m = m0 + t * 8 + (lane >> 2);
-    const int64_t k = box0 * kBox + ch * 128 + input_of<G>(w, lane & 3);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (m < a.M && k < a.K)
-      v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.A) + m * a.K + k));
-    uint4 o;  // v holds inputs 01 23 45 67
-    o.x = __byte_perm(v.x, v.z, 0x5410);  // 0 4
-    o.y = __byte_perm(v.x, v.z, 0x7632);  // 1 5
-    o.z = __byte_perm(v.y, v.w, 0x5410);  // 2 6
-    o.w = __byte_perm(v.y, v.w, 0x7632);  // 3 7
-    *reinterpret_cast<uint4*>(xs + ((size_t)t * n + ch) * kXChunk + (w * 32 + lane) * 16) = o;
+  const int n = 2 * boxes, all = NT * n * 128;
+  constexpr int U = 4;  // loads in flight together
+  for (int i0 = threadIdx.x; i0 < all; i0 += U * kThreads) {
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      const int lane = i & 31, w = (i >> 5) & 3, ch = (i >> 7) % n, t = (i >> 7) / n;
+      const int64_t m = m0 + t * 8 + (lane >> 2);
+      const int64_t k = box0 * kBox + ch * 128 + input_of<G>(w, lane & 3);
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (i < all && m < a.M && k < a.K)
+        v[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.A) + m * a.K + k));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      if (i >= all) break;
+      uint4 o;  // v holds inputs 01 23 45 67
+      o.x = __byte_perm(v[u].x, v[u].z, 0x5410);  // 0 4
+      o.y = __byte_perm(v[u].x, v[u].z, 0x7632);  // 1 5
+      o.z = __byte_perm(v[u].y, v[u].w, 0x5410);  // 2 6
+      o.w = __byte_perm(v[u].y, v[u].w, 0x7632);  // 3 7
+      *reinterpret_cast<uint4*>(xs + (size_t)i * 16) = o;  // [tile][chunk][word][lane]
+    }
+  }
+}
+
+// Outputs n .. n + 3 of token m, those there are.
+__device__ __forceinline__ void store_outputs(const W4Args& a, int64_t m, int64_t n, float4 f) {
+  float v[4] = {f.x, f.y, f.z, f.w};
+  if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n + j < a.N) v[j] += __ldg(a.bias + n + j);
+  }
+  const int64_t at = m * a.N + n;
+  if (!M3_IN(at, a.M * a.N, a.status)) return;
+  if (a.N % 4 == 0) {  // whole and aligned
+    if (a.out_f32)
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+          make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n + j < a.N) io_store(a.out, at + j, v[j], !a.out_f32);
   }
 }
 
@@ -310,6 +343,7 @@ w4_kernel(const W4Args a, const W4Plan p, const __grid_constant__ CUtensorMap ma
     return;
   }
   const int64_t m0 = (int64_t)blockIdx.y * 8 * NT;
+  const int tokens = (int)(a.M - m0 < 8 * NT ? a.M - m0 : 8 * NT);
   const bool vec = a.K % kBox == 0;
   const int part = warp % p.ks, myrb = warp / p.ks;
   const bool busy = myrb < p.rb;
@@ -395,27 +429,36 @@ w4_kernel(const W4Args a, const W4Plan p, const __grid_constant__ CUtensorMap ma
 #pragma unroll
       for (int t = 0; t < MT; ++t) pr[t] = nx[t];
     }
-    // the warps' parts of the inputs, added in order
+    // the warps' parts of the inputs, added in order, four outputs a thread
     if (busy) {
-      float* r = red + warp * kRed + output_of<G>(lane >> 2) + 16 * MT * 2 * (lane & 3);
+      float* r = red + warp * kRed + output_of<G>(lane >> 2);
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int j = 0; j < 2; ++j) {
+          const int tok = n * 8 + (lane & 3) * 2 + j;
+          if (tok >= tokens) continue;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            r[t * 16 + (i >> 1) * 8 + 16 * MT * (n * 8 + (i & 1))] = acc[t][n][i];
+          for (int t = 0; t < MT; ++t) {
+            r[16 * MT * tok + t * 16] = acc[t][n][j];
+            r[16 * MT * tok + t * 16 + 8] = acc[t][n][2 + j];
+          }
+        }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < p.rb * kRed; i += kThreads) {
-      const int st = i / kRed, o = i % kRed;
-      const int64_t n = (item * p.rb + st) * 16 * MT + o % (16 * MT), m = m0 + o / (16 * MT);
-      if (n >= a.N || m >= a.M) continue;
-      const float* r = red + st * p.ks * kRed + o;
-      float v = r[0];
-      for (int k = 1; k < p.ks; ++k) v += r[k * kRed];
-      if (a.bias) v += __ldg(a.bias + n);
-      if (M3_IN(m * a.N + n, a.M * a.N, a.status)) io_store(a.out, m * a.N + n, v, !a.out_f32);
+    constexpr int kQuads = 4 * MT;  // of a row block's outputs
+    for (int i = threadIdx.x; i < p.rb * tokens * kQuads; i += kThreads) {
+      const int qd = i % kQuads, rest = i / kQuads, tok = rest % tokens, st = rest / tokens;
+      const int64_t n = (int64_t)(item * p.rb + st) * 16 * MT + qd * 4, m = m0 + tok;
+      if (n >= a.N) continue;
+      const float* r = red + st * p.ks * kRed + 16 * MT * tok + qd * 4;
+      float4 v = *reinterpret_cast<const float4*>(r);
+#pragma unroll 4
+      for (int k = 1; k < p.ks; ++k) {
+        const float4 f = *reinterpret_cast<const float4*>(r + k * kRed);
+        v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
+      }
+      store_outputs(a, m, n, v);
     }
     if (item + (int)gridDim.x < p.items) __syncthreads();  // before the sums are overwritten
   }
@@ -980,21 +1023,8 @@ w4_tc_kernel(const W4Args a, const TcPlan p, const __grid_constant__ CUtensorMap
 #pragma unroll
         for (int k = 1; k < 8; ++k)
           if (k < p.split) v[j] += f[k][j];
-        if (a.bias && n + j < a.N) v[j] += __ldg(a.bias + n + j);
       }
-      if (!M3_IN(m * a.N + n, a.M * a.N, a.status)) continue;
-      if (n + 4 <= a.N && a.N % 4 == 0) {
-        if (a.out_f32)
-          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + m * a.N + n) =
-              make_float4(v[0], v[1], v[2], v[3]);
-        else
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + m * a.N + n) =
-              make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (n + j < a.N) io_store(a.out, m * a.N + n + j, v[j], !a.out_f32);
-      }
+      store_outputs(a, m, n, make_float4(v[0], v[1], v[2], v[3]));
     }
   }
   asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
