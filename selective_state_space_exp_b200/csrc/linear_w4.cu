@@ -56,6 +56,14 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// A constant that stays in a register: as a plain one it is moved into a new
+// register at each use.
+__device__ __forceinline__ uint32_t in_register(uint32_t v) {
+  uint32_t r;
+  asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -174,7 +182,8 @@ __device__ __forceinline__ void load_params(const uint16_t* s, const uint8_t* z,
 template <int G, bool ZEROS, int MT, int NT>
 __device__ __forceinline__ void box_products(const uint8_t* codes, const uint8_t* xs, int xstride,
                                              const Params<G> (&pr)[MT], int lane, uint32_t mask,
-                                             uint32_t magic, float (&acc)[MT][NT][4]) {
+                                             uint32_t magic, uint32_t bytes,
+                                             float (&acc)[MT][NT][4]) {
   constexpr int words = G / 32, NG = kBox / G;
   const int r = output_of<G>(lane >> 2), c = lane & 3;
   // a lane's piece of group i: byte i * G / 2 + c * G / 8 of its row, the 16-byte
@@ -209,8 +218,7 @@ __device__ __forceinline__ void box_products(const uint8_t* codes, const uint8_t
           q[t][h][0] = *reinterpret_cast<const uint32_t*>(p);
         }
         // 128 + z, twice: the zero point's byte below 0x43
-        zz[t][h] = ZEROS ? __byte_perm(zb[t][h][i / 4], 0x43434343u, 0x4040u | ((i & 3) * 0x0101u))
-                         : 0x43084308u;
+        zz[t][h] = ZEROS ? __byte_perm(zb[t][h][i / 4], bytes, 0x4040u | ((i & 3) * 0x0101u)) : bytes;
       }
     }
     float d[MT][NT][4];
@@ -322,9 +330,9 @@ struct W4Plan {
   int xboxes;   // boxes whose token values are held: all of a row's, or ks
   int items;    // groups of rb row blocks
   int all;      // boxes of a row
-  // 0x000f000f and 0x43004300: as kernel arguments they are operands from the
-  // constant bank; as literals each use first moved one into a register
-  uint32_t mask, magic;
+  // 0x000f000f (as an argument an operand from the constant bank), 0x43004300, and
+  // 0x43434343 with zero points or 128 + 8 twice without
+  uint32_t mask, magic, bytes;
 };
 
 template <int G, bool ZEROS, int MT, int NT>
@@ -373,7 +381,7 @@ w4_kernel(const W4Args a, const W4Plan p, const __grid_constant__ CUtensorMap ma
     for (int s = 0; s < p.stages; ++s) ask();
   }
   __syncwarp();
-  const uint32_t magic = p.magic;
+  const uint32_t magic = in_register(p.magic), bytes = in_register(p.bytes);
   const bool whole = p.xboxes >= p.ks * p.slices;  // all token values are held
   if (whole) {
     stage_tokens<G, NT>(a, xs, m0, 0, p.xboxes);
@@ -418,7 +426,7 @@ w4_kernel(const W4Args a, const W4Plan p, const __grid_constant__ CUtensorMap ma
       if (ok) {
         const int xb = whole ? sl * p.ks + part : part;
         box_products<G, ZEROS, MT, NT>(ring + slot * kBoxBytes, xs + (size_t)xb * 2 * kXChunk,
-                                       p.xboxes * 2 * kXChunk, pr, lane, p.mask, magic, acc);
+                                       p.xboxes * 2 * kXChunk, pr, lane, p.mask, magic, bytes, acc);
       }
       __syncwarp();  // every lane has read the slot
       if (ok && lane == 0) ask();
@@ -527,6 +535,7 @@ bool make_plan(const W4Args& a, int MT, int NT, bool whole, W4Plan* p) {
   p->all = (int)all;
   p->mask = 0x000f000fu;
   p->magic = 0x43004300u;
+  p->bytes = a.zeros ? 0x43434343u : 0x43084308u;
   p->items = (int)((rows + p->rb - 1) / p->rb);
   p->xboxes = whole ? p->ks * p->slices : p->ks;
   const int64_t left = kSmemMost - red - kWarps * kMostStages * 8 - (int64_t)p->xboxes * NT * 2 * kXChunk;
@@ -733,7 +742,7 @@ w4_tc_kernel(const W4Args a, const TcPlan p, const __grid_constant__ CUtensorMap
     const int q = warp & 3, wg = warp >> 2;
     const int r = 32 * q + lane;
     const uint32_t lane_base = (uint32_t)(32 * q) << 16;
-    const uint32_t magic = p.magic;
+    const uint32_t magic = in_register(p.magic);
     constexpr int WORDS = 32 / kWG;                   // of a row's step, a thread's part
     Turn code, at, done;                              // done: two steps behind
     uint32_t it = 0, blk = 0;                                 // blocks of scales so far
