@@ -582,7 +582,8 @@ def _addr(name, t, dtype, shape, device):
     """Address of t after checks of its type, shape, device and layout; None passes."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == device.index and
+            t.is_contiguous()):
         return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}: expected {dtype}")
@@ -593,12 +594,17 @@ def _addr(name, t, dtype, shape, device):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _scratch(like, nbytes, workspace, device):
+def _rows(n, width, dtype, device):
+    """A new [n][width] (the quickest of torch's ways to make one)."""
+    return torch.empty_strided((n, width), (width, 1), dtype=dtype, device=device)
+
+
+def _scratch(nbytes, workspace, device):
     """(address, bytes, the tensor to keep alive) of a call's workspace."""
     if workspace is None:
         if nbytes == 0:
             return None, 0, None
-        workspace = like.new_empty(nbytes, dtype=torch.uint8)
+        workspace = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
@@ -648,9 +654,9 @@ def _norm_forward(fn, plan, pre, x, stat, weight, bias, z, act, y, workspace, st
             py = y.data_ptr()
         else:
             py = _addr("y", y, dt, shape, dev)
-        mean = x.new_empty(stat, dtype=torch.float32)
-        rstd = x.new_empty(stat, dtype=torch.float32)
-        pws, nws, keep = _scratch(x, plan[1], workspace, dev)
+        mean = _rows(*stat, torch.float32, dev)
+        rstd = _rows(*stat, torch.float32, dev)
+        pws, nws, keep = _scratch(plan[1], workspace, dev)
         status = getattr(load(), fn)(*args, py, mean.data_ptr() or None, rstd.data_ptr() or None,
                                      pws, nws, st)
     finally:
@@ -683,7 +689,7 @@ def _norm_backward(fn, plan, pre, x, stat, mean, rstd, dy, weight, bias, z, act,
         if z is not None:
             g["z"] = torch.empty_like(x)
             pz = g["z"].data_ptr()
-        pws, nws, keep = _scratch(x, plan[1], workspace, dev)
+        pws, nws, keep = _scratch(plan[1], workspace, dev)
         status = getattr(load(), fn)(*args, g["x"].data_ptr() or None, g["weight"].data_ptr(),
                                      g["bias"].data_ptr(), pz, pws, nws, st)
     finally:
@@ -794,7 +800,7 @@ def m3_linear_xent_fwd(h, W, targets, *, ignore_index: int = -100, workspace=Non
     try:
         loss = torch.empty_like(targets, dtype=torch.float32)
         lse = torch.empty_like(targets, dtype=torch.float32)
-        pws, nws, keep = _scratch(h, need, workspace, dev)
+        pws, nws, keep = _scratch(need, workspace, dev)
         status = load().m3_linear_xent_fwd(*args, ignore_index, loss.data_ptr(), lse.data_ptr(),
                                            pws, nws, st)
     finally:
@@ -821,7 +827,7 @@ def m3_linear_xent_bwd(h, W, targets, lse, dloss, *, ignore_index: int = -100, w
     try:
         dh = torch.empty_like(h) if want_dh else None
         dW = torch.empty_like(W) if want_dW else None
-        pws, nws, keep = _scratch(h, need, workspace, dev)
+        pws, nws, keep = _scratch(need, workspace, dev)
         status = load().m3_linear_xent_bwd(*args, ignore_index, plse, pdl,
                                            dh.data_ptr() if want_dh else None,
                                            dW.data_ptr() if want_dW else None, pws, nws, st)
@@ -892,12 +898,14 @@ def m3_linear_w4(A, codes, scales, zeros=None, bias=None, *, out=None, out_dtype
     if ctx is not None:
         ctx.__enter__()
     try:
-        full = shape[:-1] + (N,)
-        if out is None:
-            out = A.new_empty(full, dtype=out_dtype)
+        if out is not None:
+            po = _addr("out", out, out_dtype, shape[:-1] + (N,), dev)
+        elif len(shape) == 2:
+            out = _rows(shape[0], N, out_dtype, dev)
             po = out.data_ptr()
         else:
-            po = _addr("out", out, out_dtype, full, dev)
+            out = A.new_empty(shape[:-1] + (N,), dtype=out_dtype)
+            po = out.data_ptr()
         status = load().m3_linear_w4(*args, po, code, st)
     finally:
         if ctx is not None:
