@@ -243,6 +243,8 @@ __device__ __forceinline__ int most_rows(const NormArgs& a, const UnitPlan& p) {
 
 template <bool BF16, int V, int NV, int LANES, int ACT>
 __global__ void __launch_bounds__(kThreads) unit_fwd_kernel(const NormArgs a, const UnitPlan p) {
+  let_next_start();
+  wait_for_previous();
   using X = Io<BF16, V>;
   using R = typename X::R;
   constexpr int P = X::P;
@@ -331,6 +333,8 @@ constexpr int kUnitRows = 2;  // rows whose loads are in flight together
 
 template <bool BF16, int V, int NV, int LANES, int ACT>
 __global__ void __launch_bounds__(kThreads) unit_bwd_kernel(const NormArgs a, const UnitPlan p) {
+  let_next_start();
+  wait_for_previous();
   using X = Io<BF16, V>;
   constexpr int P = X::P;
   __shared__ float2 s_red[kThreads / 32];
@@ -577,6 +581,8 @@ __device__ __forceinline__ void tile_sums(const SlicePlan& p, float2 c, float2* 
 
 template <bool BF16, int V>
 __global__ void __launch_bounds__(kThreads, 4) slice_stats_kernel(const NormArgs a, const SlicePlan p) {
+  let_next_start();
+  wait_for_previous();
   using X = Io<BF16, V>;
   const Place o = place_of(a, p);
   // sums about the group's first value in this split: it lies among the values,
@@ -619,6 +625,8 @@ __global__ void __launch_bounds__(kThreads, 4) slice_stats_kernel(const NormArgs
 // A slice's mean and 1 / deviation from its partial moments, a warp each.
 __global__ void __launch_bounds__(kThreads)
 slice_finish_kernel(const NormArgs a, int parts, int64_t slices, float2* stat) {
+  let_next_start();
+  wait_for_previous();
   const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (i >= slices) return;
@@ -636,6 +644,8 @@ slice_finish_kernel(const NormArgs a, int parts, int64_t slices, float2* stat) {
 template <bool BF16, int V, int ACT>
 __global__ void __launch_bounds__(kThreads, 4)
 slice_apply_kernel(const NormArgs a, const SlicePlan p, const float2* stat) {
+  let_next_start();
+  wait_for_previous();
   using X = Io<BF16, V>;
   const Place o = place_of(a, p);
   if (!o.on) return;
@@ -667,6 +677,8 @@ slice_apply_kernel(const NormArgs a, const SlicePlan p, const float2* stat) {
 template <bool BF16, int V, int ACT>
 __global__ void __launch_bounds__(kThreads, 3)
 slice_sums_kernel(const NormArgs a, const SlicePlan p, float2* csum, float* part) {
+  let_next_start();
+  wait_for_previous();
   using X = Io<BF16, V>;
   const Place o = place_of(a, p);
   float2 c = both(0.f), dw[X::P], db[X::P];
@@ -739,6 +751,8 @@ slice_sums_kernel(const NormArgs a, const SlicePlan p, float2* csum, float* part
 // A slice's two means from its partial sums, a warp each.
 __global__ void __launch_bounds__(kThreads)
 slice_means_kernel(const NormArgs a, int parts, int64_t slices, const float2* csum, float2* means) {
+  let_next_start();
+  wait_for_previous();
   const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (i >= slices) return;
@@ -753,6 +767,8 @@ slice_means_kernel(const NormArgs a, int parts, int64_t slices, const float2* cs
 template <bool BF16, int V, int ACT>
 __global__ void __launch_bounds__(kThreads, 3)
 slice_dx_kernel(const NormArgs a, const SlicePlan p, const float2* means) {
+  let_next_start();
+  wait_for_previous();
   using X = Io<BF16, V>;
   const Place o = place_of(a, p);
   if (!o.on) return;
@@ -787,6 +803,8 @@ slice_dx_kernel(const NormArgs a, const SlicePlan p, const float2* means) {
 // channels a block.
 __global__ void __launch_bounds__(1024)
 param_reduce_kernel(const float* part, int rows, int64_t channels, float* dw, float* db) {
+  let_next_start();
+  wait_for_previous();
   __shared__ float s[32][33];
   float* out = blockIdx.y == 0 ? dw : db;
   if (!out) return;
@@ -918,13 +936,12 @@ cudaError_t with_shape(const NormArgs& a, int V, F&& f) {
 }
 
 template <typename K, typename... Args>
-cudaError_t launch(K kernel, dim3 grid, size_t smem, cudaStream_t s, Args... args) {
+cudaError_t launch(K kernel, dim3 grid, size_t smem, cudaStream_t s, bool dependent, Args... args) {
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<grid, kThreads, smem, s>>>(args...);
-  return cudaGetLastError();
+  return launch_kernel(kernel, grid, kThreads, smem, s, dependent, 1, args...);
 }
 
 // The lanes of a unit are a compile-time number where the vectors are whole
@@ -938,8 +955,8 @@ cudaError_t unit_launch_nv(const NormArgs& a, const UnitPlan& p, bool backward, 
     constexpr int wide = V * (BF16 ? 2 : 4) == 16;
     auto go = [&](auto lanes) {
       constexpr int L = decltype(lanes)::value;
-      return backward ? launch(unit_bwd_kernel<BF16, V, NV, L, ACT>, grid, smem, s, a, p)
-                      : launch(unit_fwd_kernel<BF16, V, NV, L, ACT>, grid, 0, s, a, p);
+      return backward ? launch(unit_bwd_kernel<BF16, V, NV, L, ACT>, grid, smem, s, false, a, p)
+                      : launch(unit_fwd_kernel<BF16, V, NV, L, ACT>, grid, 0, s, false, a, p);
     };
     if (p.L == 32) return go(std::integral_constant<int, 32>());
     if constexpr (V * NV > kMaxLaneElems / 4) {  // more lanes only where fewer would hold too much
@@ -971,9 +988,8 @@ cudaError_t unit_launch(const NormArgs& a, const UnitPlan& p, bool backward, cud
 }
 
 cudaError_t param_reduce(const NormArgs& a, const float* part, int64_t rows, cudaStream_t s) {
-  param_reduce_kernel<<<dim3((unsigned)((a.channels + 31) / 32), 2), 1024, 0, s>>>(
-      part, (int)rows, a.channels, a.dw, a.db);
-  return cudaGetLastError();
+  return launch_kernel(param_reduce_kernel, dim3((unsigned)((a.channels + 31) / 32), 2), 1024, 0, s, true, 1,
+                       part, (int)rows, a.channels, a.dw, a.db);
 }
 
 }  // namespace
@@ -998,11 +1014,11 @@ cudaError_t group_norm_fwd_launch(const NormArgs& a0, cudaStream_t s) {
   return with_shape(a, p.V, [&](auto bf16, auto v, auto act) {
     constexpr bool B = decltype(bf16)::value;
     constexpr int V = decltype(v)::value, A = decltype(act)::value;
-    cudaError_t e = launch(slice_stats_kernel<B, V>, grid, 0, s, a, p);
+    cudaError_t e = launch(slice_stats_kernel<B, V>, grid, 0, s, false, a, p);
     if (e == cudaSuccess)
       e = launch(slice_finish_kernel, dim3((unsigned)((slices + kThreads / 32 - 1) / (kThreads / 32))), 0, s,
-                 a, p.splits * p.pieces, slices, stat);
-    return e != cudaSuccess ? e : launch(slice_apply_kernel<B, V, A>, grid, 0, s, a, p, (const float2*)stat);
+                 true, a, p.splits * p.pieces, slices, stat);
+    return e != cudaSuccess ? e : launch(slice_apply_kernel<B, V, A>, grid, 0, s, true, a, p, (const float2*)stat);
   });
 }
 
@@ -1026,11 +1042,11 @@ cudaError_t group_norm_bwd_launch(const NormArgs& a0, cudaStream_t s) {
   const cudaError_t e = with_shape(a, p.V, [&](auto bf16, auto v, auto act) {
     constexpr bool B = decltype(bf16)::value;
     constexpr int V = decltype(v)::value, A = decltype(act)::value;
-    cudaError_t r = launch(slice_sums_kernel<B, V, A>, grid, smem, s, a, p, csum, rows);
+    cudaError_t r = launch(slice_sums_kernel<B, V, A>, grid, smem, s, false, a, p, csum, rows);
     if (r != cudaSuccess || !a.dx) return r;
-    r = launch(slice_means_kernel, dim3((unsigned)((slices + kThreads / 32 - 1) / (kThreads / 32))), 0, s, a,
+    r = launch(slice_means_kernel, dim3((unsigned)((slices + kThreads / 32 - 1) / (kThreads / 32))), 0, s, true, a,
                p.splits * p.pieces, slices, (const float2*)csum, means);
-    return r != cudaSuccess ? r : launch(slice_dx_kernel<B, V, A>, grid, 0, s, a, p, (const float2*)means);
+    return r != cudaSuccess ? r : launch(slice_dx_kernel<B, V, A>, grid, 0, s, true, a, p, (const float2*)means);
   });
   return e != cudaSuccess || !params ? e : param_reduce(a, rows, a.batch * p.splits, s);
 }

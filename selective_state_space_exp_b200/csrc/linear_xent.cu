@@ -71,6 +71,7 @@ struct GemmArgs {
   int64_t M, N;           // extent of the output
   int kb, kb_per;         // reduction blocks in all, and of one split
   int cg, mt, nt, splits; // CTAs of a tile; tiles
+  bool dependent;         // not the call's first kernel
   int* status;
   // stats, dlogits: rows are tokens, columns classes v0 + n
   const int64_t* targets;
@@ -364,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
   using C = Cfg<CG>;
   constexpr int kStages = C::STAGES;
+  let_next_start();
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sbase = smem_u32(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -402,6 +404,7 @@ xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = *s_tmem;
+  wait_for_previous();
 
   if (warp == 0 && lane == 0) {
     uint32_t it = 0;
@@ -509,6 +512,8 @@ __global__ void __launch_bounds__(kJoinThreads)
 xent_join_kernel(const float2* stat, int parts, int64_t M, int64_t V, const int64_t* targets,
                  int64_t ignore, const float* tlogit, float* loss, float* lse, int* status) {
   constexpr int kRows = kJoinThreads / kJoinTokens;
+  let_next_start();
+  wait_for_previous();
   __shared__ float2 s[kRows][kJoinTokens];
   const int t = threadIdx.x % kJoinTokens, w = threadIdx.x / kJoinTokens;
   const int64_t m = (int64_t)blockIdx.x * kJoinTokens + t;
@@ -543,6 +548,8 @@ xent_join_kernel(const float2* stat, int parts, int64_t M, int64_t V, const int6
 // out = c times the sum over splits of part[s], rounded to bf16; n is a multiple of 8.
 __global__ void __launch_bounds__(256)
 xent_sum_kernel(const float* part, int splits, int64_t n, const float* unit, __nv_bfloat16* out) {
+  let_next_start();
+  wait_for_previous();
   const float c = *unit;
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n;
        i += (int64_t)gridDim.x * 1024) {
@@ -611,20 +618,8 @@ cudaError_t gemm_cg(const GemmArgs& g, const Operand& a, const Operand& b, cudaS
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)g.mt * g.nt * g.splits;
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)(CG * (tiles < sms / CG ? tiles : sms / CG)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CG;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = CG > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, g, maps);
+  return launch_kernel(kern, dim3((unsigned)(CG * (tiles < sms / CG ? tiles : sms / CG))), kThreads,
+                       C::SMEM, s, g.dependent, CG, g, maps);
 }
 
 template <int MODE, bool AMN, bool BMN>
@@ -692,9 +687,8 @@ size_t fwd_stat_bytes(const XentArgs& a) {
 cudaError_t sum_splits(const float* part, int splits, int64_t n, const float* unit, void* out,
                        cudaStream_t s) {
   const int64_t blocks = ceil_div(n, 1024);
-  xent_sum_kernel<<<(unsigned)(blocks < kPlanSms * 8 ? blocks : kPlanSms * 8), 256, 0, s>>>(
-      part, splits, n, unit, static_cast<__nv_bfloat16*>(out));
-  return cudaGetLastError();
+  return launch_kernel(xent_sum_kernel, dim3((unsigned)(blocks < kPlanSms * 8 ? blocks : kPlanSms * 8)),
+                       256, 0, s, true, 1, part, splits, n, unit, static_cast<__nv_bfloat16*>(out));
 }
 
 }  // namespace
@@ -719,9 +713,9 @@ cudaError_t xent_fwd_launch(const XentArgs& a, cudaStream_t s) {
   cudaError_t e = gemm<kStats, false, false>(g, Operand{a.h, a.M, a.K, a.K},
                                              Operand{a.W, a.V, a.K, a.K}, s);
   if (e != cudaSuccess) return e;
-  xent_join_kernel<<<(unsigned)ceil_div(a.M, kJoinTokens), kJoinThreads, 0, s>>>(
-      g.stat, 2 * g.nt, a.M, a.V, a.targets, a.ignore, g.tlogit, a.loss, a.lse, a.status);
-  return cudaGetLastError();
+  return launch_kernel(xent_join_kernel, dim3((unsigned)ceil_div(a.M, kJoinTokens)), kJoinThreads, 0, s,
+                       true, 1, (const float2*)g.stat, 2 * g.nt, a.M, a.V, a.targets, a.ignore,
+                       (const float*)g.tlogit, a.loss, a.lse, a.status);
 }
 
 cudaError_t xent_bwd_launch(const XentArgs& a, cudaStream_t s) {
@@ -736,6 +730,7 @@ cudaError_t xent_bwd_launch(const XentArgs& a, cudaStream_t s) {
     GemmArgs g;
     memset(&g, 0, sizeof(g));
     set_tiles(&g, a.M, n, a.K, 1);
+    g.dependent = i > 0;
     g.status = a.status;
     g.targets = a.targets;
     g.ignore = a.ignore;
@@ -753,6 +748,7 @@ cudaError_t xent_bwd_launch(const XentArgs& a, cudaStream_t s) {
       GemmArgs w;
       memset(&w, 0, sizeof(w));
       set_tiles(&w, n, a.K, a.M, p.dw_splits);
+      w.dependent = true;
       w.status = a.status;
       w.unit = unit;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dW) + v0 * a.K;
@@ -765,6 +761,7 @@ cudaError_t xent_bwd_launch(const XentArgs& a, cudaStream_t s) {
       GemmArgs h;
       memset(&h, 0, sizeof(h));
       set_tiles(&h, a.M, a.K, n, p.dh_splits);
+      h.dependent = true;
       h.status = a.status;
       h.unit = unit;
       const bool last = i + 1 == p.pieces;

@@ -12,6 +12,44 @@ namespace m3 {
 // sizing a workspace needs no device.
 constexpr int kPlanSms = 148;
 
+// The kernels of one call follow each other as programmatic dependents: each
+// lets the next one start (its blocks set up on SMs that are free), and waits for
+// the one before to be complete, and its writes visible, before it touches global
+// memory.  Every kernel of a call does both, so the order is that of the stream.
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Launches a kernel; dependent: as a programmatic dependent of the kernel before
+// it in the stream (one of the same call); cluster: blocks of a cluster along x.
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                          bool dependent, int cluster, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2] = {};
+  int n = 0;
+  if (dependent) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = (unsigned)cluster;
+    at[n].val.clusterDim.y = 1;
+    at[n++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = (unsigned)n;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // Device address of the library's error word (m3_api.cu).
 int device_status_word(int** out);
 
