@@ -330,6 +330,10 @@ __global__ void __launch_bounds__(kThreads) unit_fwd_kernel(const NormArgs a, co
 }
 
 constexpr int kUnitRows = 2;  // rows whose loads are in flight together
+// Rows of a row slot that one block takes alone in the backward: it then leaves dw
+// and db themselves (8 x 4096, 64 groups: 8.0 us for 8 rows by one block, against
+// 6.1 us by several and a second kernel that adds their sums; 2 rows: 2.7 us).
+constexpr int kOneBlockRows = 4;
 
 template <bool BF16, int V, int NV, int LANES, int ACT>
 __global__ void __launch_bounds__(kThreads) unit_bwd_kernel(const NormArgs a, const UnitPlan p) {
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(kThreads) unit_bwd_kernel(const NormArgs a, co
     at += kUnitRows * step;
     stat += kUnitRows * o.sstep;
   }
-  if (!a.ws) return;
+  if (!a.part_w && !a.part_b) return;
   // the block's sums over its rows: row slots are added in shared memory
   extern __shared__ float s_sum[];  // [ty][ub * cg] twice
   const int width = p.ub * (int)a.cg;
@@ -433,7 +437,6 @@ __global__ void __launch_bounds__(kThreads) unit_bwd_kernel(const NormArgs a, co
     }
   }
   __syncthreads();
-  float* part = reinterpret_cast<float*>(a.ws);  // [2][gridDim.y][channels]
   for (int i = threadIdx.x; i < width; i += kThreads) {
     const int64_t c = (int64_t)blockIdx.x * width + i;
     if (c >= a.channels) break;
@@ -442,8 +445,8 @@ __global__ void __launch_bounds__(kThreads) unit_bwd_kernel(const NormArgs a, co
       tw += s_sum[r * width + i];
       tb += s_sum[(p.ty + r) * width + i];
     }
-    part[(int64_t)blockIdx.y * a.channels + c] = tw;
-    part[((int64_t)gridDim.y + blockIdx.y) * a.channels + c] = tb;
+    if (a.part_w) a.part_w[(int64_t)blockIdx.y * a.channels + c] = tw;
+    if (a.part_b) a.part_b[(int64_t)blockIdx.y * a.channels + c] = tb;
   }
 }
 
@@ -490,11 +493,22 @@ struct SlicePlan {
   int pieces;  // tiles of a group, where one does not fit a block
   int tiles;   // of a row
   int splits;
+  bool whole;  // a block takes all rows of its sample and makes both passes
 };
 
 // Rows whose loads are in flight together; fewer in the backward, where three
 // blocks an SM do better than two (both passes 79 us against 85 at 8 x 2048 x 2048).
 constexpr int kRowsAhead = 4, kBwdRowsAhead = 2;
+
+// A block makes both passes over all rows of its sample where a thread has at most
+// this many: one launch and no partial sums, but fewer blocks.  Forward / backward
+// with SiLU, us, this form against splits: 4 x 128 x 2048 in bf16 (8 rows a thread)
+// 4.6 / 7.5 against 9.6 / 16.3; 16 x 256 x 2048 (32) 11.6 / 21.0 against 18.9 / 30.7;
+// 16 x 512 x 2048 (64) 19.7 / 45.9 against 25.0 / 50.6; 6 x 160 x 2400 (54) 8.4 / 19.5
+// against 11.2 / 17.9; 64 x 256 x 2048 (128) 51.8 / 110 against 47.7 / 89.6.  More rows
+// are in flight than above, for the blocks are few.
+constexpr int kWholeRows = 32;
+constexpr int kWholeAhead = 8, kWholeBwdAhead = 4;
 
 __device__ __forceinline__ void split_rows(const Chain& c, int splits, int64_t& r0, int64_t& r1) {
   const int64_t per = ((uint32_t)c.len + (uint32_t)splits - 1) / (uint32_t)splits;
@@ -579,12 +593,11 @@ __device__ __forceinline__ void tile_sums(const SlicePlan& p, float2 c, float2* 
   }
 }
 
-template <bool BF16, int V>
-__global__ void __launch_bounds__(kThreads, 4) slice_stats_kernel(const NormArgs a, const SlicePlan p) {
-  let_next_start();
-  wait_for_previous();
+// The moments of each group of the tile over the block's rows: f(group of the tile,
+// group, moments).
+template <bool BF16, int V, int AHEAD, typename F>
+__device__ __forceinline__ void stats_pass(const NormArgs& a, const SlicePlan& p, const Place& o, F&& f) {
   using X = Io<BF16, V>;
-  const Place o = place_of(a, p);
   // sums about the group's first value in this split: it lies among the values,
   // so the squares cannot be lost under it
   float2 s1 = both(0.f), s2 = both(0.f);
@@ -594,14 +607,14 @@ __global__ void __launch_bounds__(kThreads, 4) slice_stats_kernel(const NormArgs
   };
   if (o.on) {
     const float pivot = pivot_of(group_of(a, p, o, o.group));
-    typename X::R raw[kRowsAhead];
-    over_rows<kRowsAhead>(a, p, o, [&](int u, int64_t at) { raw[u] = X::load(a.x, at); },
+    typename X::R raw[AHEAD];
+    over_rows<AHEAD>(a, p, o, [&](int u, int64_t at) { raw[u] = X::load(a.x, at); },
                           [&](int u, int64_t) {
-                            float2 f[X::P];
-                            X::unpack(raw[u], f);
+                            float2 v[X::P];
+                            X::unpack(raw[u], v);
 #pragma unroll
                             for (int e = 0; e < X::P; ++e) {
-                              const float2 d = minus<V>(f[e], pivot);
+                              const float2 d = minus<V>(v[e], pivot);
                               s1 = fadd2(s1, d);
                               s2 = ffma2(d, d, s2);
                             }
@@ -616,9 +629,26 @@ __global__ void __launch_bounds__(kThreads, 4) slice_stats_kernel(const NormArgs
     const int64_t vecs = p.pieces > 1 ? (nvec - first < p.tx ? nvec - first : p.tx) : nvec;
     const float n = (float)((o.r1 - o.r0) * vecs * V);
     const float d = n > 0.f ? c.x / n : 0.f;
-    Moments* out = reinterpret_cast<Moments*>(a.ws);
-    out[((o.sample * a.groups + g) * p.splits + blockIdx.y) * p.pieces + o.piece] =
-        Moments{n, pivot_of(g) + d, fmaf(-d, c.x, c.y)};
+    f(i, g, Moments{n, pivot_of(g) + d, fmaf(-d, c.x, c.y)});
+  });
+}
+
+// A slice's mean and 1 / deviation, also for the caller.
+__device__ __forceinline__ float2 finish_stats(const NormArgs& a, int64_t slice, const Moments& m) {
+  const float rstd = m.n > 0.f ? rsqrtf(m.m2 / m.n + a.eps) : 0.f;
+  if (a.mean) a.mean[slice] = m.mean;
+  if (a.rstd) a.rstd[slice] = rstd;
+  return make_float2(m.mean, rstd);
+}
+
+template <bool BF16, int V>
+__global__ void __launch_bounds__(kThreads, 4) slice_stats_kernel(const NormArgs a, const SlicePlan p) {
+  let_next_start();
+  wait_for_previous();
+  const Place o = place_of(a, p);
+  Moments* out = reinterpret_cast<Moments*>(a.ws);
+  stats_pass<BF16, V, kRowsAhead>(a, p, o, [&](int, int64_t g, const Moments& m) {
+    out[((o.sample * a.groups + g) * p.splits + blockIdx.y) * p.pieces + o.piece] = m;
   });
 }
 
@@ -634,29 +664,21 @@ slice_finish_kernel(const NormArgs a, int parts, int64_t slices, float2* stat) {
   Moments m{0.f, 0.f, 0.f};
   for (int k = lane; k < parts; k += 32) m = merge(m, in[k]);
   m = shfl_merge(m);
-  if (lane != 0) return;
-  const float rstd = m.n > 0.f ? rsqrtf(m.m2 / m.n + a.eps) : 0.f;
-  stat[i] = make_float2(m.mean, rstd);
-  if (a.mean) a.mean[i] = m.mean;
-  if (a.rstd) a.rstd[i] = rstd;
+  if (lane == 0) stat[i] = finish_stats(a, i, m);
 }
 
-template <bool BF16, int V, int ACT>
-__global__ void __launch_bounds__(kThreads, 4)
-slice_apply_kernel(const NormArgs a, const SlicePlan p, const float2* stat) {
-  let_next_start();
-  wait_for_previous();
+// y of the block's rows, st: the mean and 1 / deviation of the thread's group.
+template <bool BF16, int V, int ACT, int AHEAD>
+__device__ __forceinline__ void apply_pass(const NormArgs& a, const SlicePlan& p, const Place& o,
+                                           const float2 st) {
   using X = Io<BF16, V>;
-  const Place o = place_of(a, p);
-  if (!o.on) return;
-  const float2 st = stat[o.sample * a.groups + group_of(a, p, o, o.group)];
   const float mean = st.x;
   float2 w[X::P], b[X::P];
   load_params<V>(a, o.col, true, w, b);
 #pragma unroll
   for (int e = 0; e < X::P; ++e) w[e] = fmul2(w[e], both(st.y));
-  typename X::R xr[kRowsAhead], zr[kRowsAhead];
-  over_rows<kRowsAhead>(a, p, o,
+  typename X::R xr[AHEAD], zr[AHEAD];
+  over_rows<AHEAD>(a, p, o,
             [&](int u, int64_t at) {
               xr[u] = X::load(a.x, at);
               if constexpr (ACT == M3_ACT_GATE) zr[u] = X::load(a.z, at);
@@ -672,15 +694,35 @@ slice_apply_kernel(const NormArgs a, const SlicePlan p, const float2* stat) {
             });
 }
 
-// Backward, first pass: the groups' two sums (one partial per split and piece),
-// the block's share of dw, db (one row of partials per sample and split), and dz.
 template <bool BF16, int V, int ACT>
-__global__ void __launch_bounds__(kThreads, 3)
-slice_sums_kernel(const NormArgs a, const SlicePlan p, float2* csum, float* part) {
+__global__ void __launch_bounds__(kThreads, 4)
+slice_apply_kernel(const NormArgs a, const SlicePlan p, const float2* stat) {
   let_next_start();
   wait_for_previous();
-  using X = Io<BF16, V>;
   const Place o = place_of(a, p);
+  if (o.on) apply_pass<BF16, V, ACT, kRowsAhead>(a, p, o, stat[o.sample * a.groups + group_of(a, p, o, o.group)]);
+}
+
+// Both passes by one block a tile, for samples of few rows.
+template <bool BF16, int V, int ACT>
+__global__ void __launch_bounds__(kThreads) whole_fwd_kernel(const NormArgs a, const SlicePlan p) {
+  let_next_start();
+  wait_for_previous();
+  const Place o = place_of(a, p);
+  __shared__ float2 s_stat[kThreads];
+  stats_pass<BF16, V, kWholeAhead>(a, p, o, [&](int i, int64_t g, const Moments& m) {
+    s_stat[i] = finish_stats(a, o.sample * a.groups + g, m);
+  });
+  __syncthreads();
+  if (o.on) apply_pass<BF16, V, ACT, kWholeAhead>(a, p, o, s_stat[o.group]);
+}
+
+// Backward, first pass: the groups' two sums over the block's rows (f(group of the
+// tile, group, sums)), the block's share of dw, db (one row of partials per sample
+// and split), and dz.
+template <bool BF16, int V, int ACT, int AHEAD, typename F>
+__device__ __forceinline__ void sums_pass(const NormArgs& a, const SlicePlan& p, const Place& o, F&& f) {
+  using X = Io<BF16, V>;
   float2 c = both(0.f), dw[X::P], db[X::P];
 #pragma unroll
   for (int e = 0; e < X::P; ++e) dw[e] = db[e] = both(0.f);
@@ -689,8 +731,8 @@ slice_sums_kernel(const NormArgs a, const SlicePlan p, float2* csum, float* part
     const float mean = __ldg(a.mean + g), rstd = __ldg(a.rstd + g);
     float2 w[X::P], b[X::P];
     load_params<V>(a, o.col, true, w, b);
-    typename X::R xr[kBwdRowsAhead], yr[kBwdRowsAhead], zr[kBwdRowsAhead];
-    over_rows<kBwdRowsAhead>(a, p, o,
+    typename X::R xr[AHEAD], yr[AHEAD], zr[AHEAD];
+    over_rows<AHEAD>(a, p, o,
               [&](int u, int64_t at) {
                 xr[u] = X::load(a.x, at);
                 yr[u] = X::load(a.dy, at);
@@ -722,7 +764,8 @@ slice_sums_kernel(const NormArgs a, const SlicePlan p, float2* csum, float* part
   __shared__ float2 s_c[kThreads];
   extern __shared__ float s_col[];  // [2][ty][tx * V], for dw and db
   const int width = p.tx * V;
-  if (part && o.ty < p.ty) {
+  const bool params = a.part_w || a.part_b;
+  if (params && o.ty < p.ty) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       s_col[o.ty * width + o.tx * V + e] = (e & 1) ? dw[e / 2].y : dw[e / 2].x;
@@ -731,21 +774,37 @@ slice_sums_kernel(const NormArgs a, const SlicePlan p, float2* csum, float* part
   }
   tile_sums(p, c, s_c, [&](int i, float2 v) {
     const int64_t g = group_of(a, p, o, i);
-    if (g < a.groups)
-      csum[((o.sample * a.groups + g) * p.splits + blockIdx.y) * p.pieces + o.piece] = v;
+    if (g < a.groups) f(i, g, v);
   });
-  if (!part) return;
+  if (!params) return;
   // columns of the tile: the first of its channels, and how many there are
   const int64_t c0 = o.col - (int64_t)o.tx * V;
   const int64_t end = p.pieces > 1 ? (o.tile / p.pieces + 1) * a.cg : a.channels;
-  const int64_t prow = o.sample * p.splits + blockIdx.y, prows = a.batch * p.splits;
+  const int64_t prow = o.sample * p.splits + blockIdx.y;
   for (int i = threadIdx.x; i < 2 * width; i += kThreads) {
     const int which = i >= width, j = i - which * width;
-    if (c0 + j >= end) continue;
+    float* part = which ? a.part_b : a.part_w;
+    if (!part || c0 + j >= end) continue;
     float v = 0.f;
     for (int r = 0; r < p.ty; ++r) v += s_col[(which * p.ty + r) * width + j];
-    part[(which * prows + prow) * a.channels + c0 + j] = v;
+    part[prow * a.channels + c0 + j] = v;
   }
+}
+
+template <bool BF16, int V, int ACT>
+__global__ void __launch_bounds__(kThreads, 3)
+slice_sums_kernel(const NormArgs a, const SlicePlan p, float2* csum) {
+  let_next_start();
+  wait_for_previous();
+  const Place o = place_of(a, p);
+  sums_pass<BF16, V, ACT, kBwdRowsAhead>(a, p, o, [&](int, int64_t g, float2 c) {
+    csum[((o.sample * a.groups + g) * p.splits + blockIdx.y) * p.pieces + o.piece] = c;
+  });
+}
+
+// Values of a slice of `rows` positions.
+__device__ __forceinline__ float values_of(const NormArgs& a, int64_t rows) {
+  return (float)((double)rows * (double)a.cg);
 }
 
 // A slice's two means from its partial sums, a warp each.
@@ -759,26 +818,22 @@ slice_means_kernel(const NormArgs a, int parts, int64_t slices, const float2* cs
   float2 c = both(0.f);
   for (int k = lane; k < parts; k += 32) c = fadd2(c, csum[i * parts + k]);
   c = make_float2(lane_sum(c.x, 32), lane_sum(c.y, 32));
-  const float n = (float)((double)rows_of(a, i / a.groups).len * (double)a.cg);
+  const float n = values_of(a, rows_of(a, i / a.groups).len);
   if (lane == 0) means[i] = make_float2(c.x / n, c.y / n);
 }
 
-// Backward, second pass: dx.
-template <bool BF16, int V, int ACT>
-__global__ void __launch_bounds__(kThreads, 3)
-slice_dx_kernel(const NormArgs a, const SlicePlan p, const float2* means) {
-  let_next_start();
-  wait_for_previous();
+// Backward, second pass: dx of the block's rows, c: the two means of the thread's group.
+template <bool BF16, int V, int ACT, int AHEAD>
+__device__ __forceinline__ void dx_pass(const NormArgs& a, const SlicePlan& p, const Place& o,
+                                        const float2 c) {
   using X = Io<BF16, V>;
-  const Place o = place_of(a, p);
-  if (!o.on) return;
   const int64_t g = o.sample * a.groups + group_of(a, p, o, o.group);
   const float mean = __ldg(a.mean + g), rstd = __ldg(a.rstd + g);
-  const float2 c = means[g], k1 = both(-c.x * rstd), k2 = both(-c.y * rstd);
+  const float2 k1 = both(-c.x * rstd), k2 = both(-c.y * rstd);
   float2 w[X::P], b[X::P];
   load_params<V>(a, o.col, true, w, b);
-  typename X::R xr[kBwdRowsAhead], yr[kBwdRowsAhead], zr[kBwdRowsAhead];
-  over_rows<kBwdRowsAhead>(a, p, o,
+  typename X::R xr[AHEAD], yr[AHEAD], zr[AHEAD];
+  over_rows<AHEAD>(a, p, o,
             [&](int u, int64_t at) {
               xr[u] = X::load(a.x, at);
               yr[u] = X::load(a.dy, at);
@@ -797,6 +852,30 @@ slice_dx_kernel(const NormArgs a, const SlicePlan p, const float2* means) {
               }
               if (M3_IN(at + V - 1, a.total_tokens * a.channels, a.status)) X::store(a.dx, at, dx);
             });
+}
+
+template <bool BF16, int V, int ACT>
+__global__ void __launch_bounds__(kThreads, 3)
+slice_dx_kernel(const NormArgs a, const SlicePlan p, const float2* means) {
+  let_next_start();
+  wait_for_previous();
+  const Place o = place_of(a, p);
+  if (o.on) dx_pass<BF16, V, ACT, kBwdRowsAhead>(a, p, o, means[o.sample * a.groups + group_of(a, p, o, o.group)]);
+}
+
+// Both passes by one block a tile.
+template <bool BF16, int V, int ACT>
+__global__ void __launch_bounds__(kThreads) whole_bwd_kernel(const NormArgs a, const SlicePlan p) {
+  let_next_start();
+  wait_for_previous();
+  const Place o = place_of(a, p);
+  const float n = values_of(a, o.r1);
+  __shared__ float2 s_mean[kThreads];
+  sums_pass<BF16, V, ACT, kWholeBwdAhead>(a, p, o, [&](int i, int64_t, float2 c) {
+    s_mean[i] = make_float2(c.x / n, c.y / n);
+  });
+  __syncthreads();
+  if (o.on && a.dx) dx_pass<BF16, V, ACT, kWholeBwdAhead>(a, p, o, s_mean[o.group]);
 }
 
 // dw (blockIdx.y = 0) or db: the rows of partials added in a fixed order, 32
@@ -863,6 +942,8 @@ bool unit_plan(const NormArgs& a, bool backward, UnitPlan* p) {
   // each leaves a row of partial sums
   const int64_t want = (int64_t)kPlanSms * (backward ? 4 : 8);
   int64_t yb = (want + p->xb - 1) / p->xb;
+  // a few rows: by one block, whose sums are dw and db
+  if (backward && a.batch <= kOneBlockRows * p->ty) yb = 1;
   const int64_t most = (a.batch + p->ty - 1) / p->ty;
   if (yb > most) yb = most;
   if (yb > 65535) yb = 65535;
@@ -870,8 +951,11 @@ bool unit_plan(const NormArgs& a, bool backward, UnitPlan* p) {
   return true;
 }
 
+int64_t rows_a_thread(const NormArgs& a, const SlicePlan& p) { return (a.seqlen + p.ty - 1) / p.ty; }
+
 SlicePlan slice_plan(const NormArgs& a, bool backward) {
   SlicePlan p;
+  p.whole = false;
   p.V = vec_elems(a);
   const int64_t nvec = a.cg / p.V;
   p.pieces = (int)((nvec + kThreads - 1) / kThreads);
@@ -895,11 +979,28 @@ SlicePlan slice_plan(const NormArgs& a, bool backward) {
   if (s > most) s = most;
   if (s > 1024) s = 1024;
   p.splits = (int)(s < 1 ? 1 : s);
-  return p;
+  if (p.pieces > 1) return p;
+  // a block for a tile of a whole sample: fewer groups a tile while SMs are idle
+  SlicePlan w = p;
+  w.splits = 1;
+  while (w.gpt > 1 && rows_a_thread(a, w) > kRowsAhead && a.batch * w.tiles * 2 <= kPlanSms) {
+    w.gpt = (w.gpt + 1) / 2;
+    w.tx = (int)(w.gpt * nvec);
+    w.ty = kThreads / w.tx;
+    w.tiles = (int)((a.groups + w.gpt - 1) / w.gpt);
+  }
+  w.whole = true;
+  return rows_a_thread(a, w) <= kWholeRows ? w : p;
 }
 
-size_t unit_bwd_bytes(const NormArgs& a, const UnitPlan& p) {
-  return (size_t)2 * p.yb * a.channels * 4;
+// Rows of partial sums for dw and db; a single row is dw and db themselves.
+size_t part_bytes(const NormArgs& a, int64_t rows) {
+  return rows > 1 ? (size_t)2 * rows * a.channels * 4 : 0;
+}
+void set_parts(NormArgs* a, int64_t rows, char* ws) {
+  if (!a->dw && !a->db) return;
+  a->part_w = rows > 1 ? reinterpret_cast<float*>(ws) : a->dw;
+  a->part_b = rows > 1 ? a->part_w + rows * a->channels : a->db;
 }
 
 size_t slice_stat_bytes(const NormArgs& a) {
@@ -951,7 +1052,7 @@ cudaError_t unit_launch_nv(const NormArgs& a, const UnitPlan& p, bool backward, 
   const dim3 grid((unsigned)p.xb, (unsigned)p.yb);
   if constexpr (V * NV > kMaxLaneElems) return cudaErrorInvalidValue;
   else {
-    const size_t smem = backward && a.ws ? (size_t)2 * p.ty * p.ub * a.cg * 4 : 0;
+    const size_t smem = backward && (a.part_w || a.part_b) ? (size_t)2 * p.ty * p.ub * a.cg * 4 : 0;
     constexpr int wide = V * (BF16 ? 2 : 4) == 16;
     auto go = [&](auto lanes) {
       constexpr int L = decltype(lanes)::value;
@@ -987,19 +1088,21 @@ cudaError_t unit_launch(const NormArgs& a, const UnitPlan& p, bool backward, cud
   });
 }
 
-cudaError_t param_reduce(const NormArgs& a, const float* part, int64_t rows, cudaStream_t s) {
+cudaError_t param_reduce(const NormArgs& a, int64_t rows, cudaStream_t s) {
+  if (rows == 1 || !a.part_w) return cudaSuccess;
   return launch_kernel(param_reduce_kernel, dim3((unsigned)((a.channels + 31) / 32), 2), 1024, 0, s, true, 1,
-                       part, (int)rows, a.channels, a.dw, a.db);
+                       (const float*)a.part_w, (int)rows, a.channels, a.dw, a.db);
 }
 
 }  // namespace
 
 size_t group_norm_workspace(const NormArgs& a, bool backward) {
   UnitPlan u;
-  if (unit_plan(a, backward, &u)) return backward ? unit_bwd_bytes(a, u) : 0;
+  if (unit_plan(a, backward, &u)) return backward ? part_bytes(a, u.yb) : 0;
   const SlicePlan p = slice_plan(a, backward);
-  if (!backward) return slice_stat_bytes(a) + (size_t)a.batch * a.groups * p.splits * p.pieces * sizeof(Moments);
-  return slice_stat_bytes(a) + slice_csum_bytes(a, p) + (size_t)2 * a.batch * p.splits * a.channels * 4;
+  if (!backward)
+    return p.whole ? 0 : slice_stat_bytes(a) + (size_t)a.batch * a.groups * p.splits * p.pieces * sizeof(Moments);
+  return (p.whole ? 0 : slice_stat_bytes(a) + slice_csum_bytes(a, p)) + part_bytes(a, a.batch * p.splits);
 }
 
 cudaError_t group_norm_fwd_launch(const NormArgs& a0, cudaStream_t s) {
@@ -1008,6 +1111,11 @@ cudaError_t group_norm_fwd_launch(const NormArgs& a0, cudaStream_t s) {
   if (unit_plan(a, false, &u)) return unit_launch(a, u, false, s);
   const SlicePlan p = slice_plan(a, false);
   const dim3 grid((unsigned)(a.batch * p.tiles), (unsigned)p.splits);
+  if (p.whole)
+    return with_shape(a, p.V, [&](auto bf16, auto v, auto act) {
+      return launch(whole_fwd_kernel<decltype(bf16)::value, decltype(v)::value, decltype(act)::value>,
+                    grid, 0, s, false, a, p);
+    });
   const int64_t slices = a.batch * a.groups;
   float2* stat = reinterpret_cast<float2*>(a.ws);
   a.ws += slice_stat_bytes(a);
@@ -1027,28 +1135,28 @@ cudaError_t group_norm_bwd_launch(const NormArgs& a0, cudaStream_t s) {
   UnitPlan u;
   const bool params = a.dw || a.db;
   if (unit_plan(a, true, &u)) {
-    const float* part = reinterpret_cast<const float*>(a.ws);
-    if (!params) a.ws = nullptr;
+    set_parts(&a, u.yb, a.ws);
     const cudaError_t e = unit_launch(a, u, true, s);
-    return e != cudaSuccess || !params ? e : param_reduce(a, part, u.yb, s);
+    return e != cudaSuccess ? e : param_reduce(a, u.yb, s);
   }
   const SlicePlan p = slice_plan(a, true);
   const dim3 grid((unsigned)(a.batch * p.tiles), (unsigned)p.splits);
   const int64_t slices = a.batch * a.groups;
   float2* means = reinterpret_cast<float2*>(a.ws);
   float2* csum = reinterpret_cast<float2*>(a.ws + slice_stat_bytes(a));
-  float* rows = params ? reinterpret_cast<float*>(a.ws + slice_stat_bytes(a) + slice_csum_bytes(a, p)) : nullptr;
+  set_parts(&a, a.batch * p.splits, p.whole ? a.ws : a.ws + slice_stat_bytes(a) + slice_csum_bytes(a, p));
   const size_t smem = params ? (size_t)2 * p.ty * p.tx * p.V * 4 : 0;
   const cudaError_t e = with_shape(a, p.V, [&](auto bf16, auto v, auto act) {
     constexpr bool B = decltype(bf16)::value;
     constexpr int V = decltype(v)::value, A = decltype(act)::value;
-    cudaError_t r = launch(slice_sums_kernel<B, V, A>, grid, smem, s, false, a, p, csum, rows);
+    if (p.whole) return launch(whole_bwd_kernel<B, V, A>, grid, smem, s, false, a, p);
+    cudaError_t r = launch(slice_sums_kernel<B, V, A>, grid, smem, s, false, a, p, csum);
     if (r != cudaSuccess || !a.dx) return r;
     r = launch(slice_means_kernel, dim3((unsigned)((slices + kThreads / 32 - 1) / (kThreads / 32))), 0, s, true, a,
                p.splits * p.pieces, slices, (const float2*)csum, means);
     return r != cudaSuccess ? r : launch(slice_dx_kernel<B, V, A>, grid, 0, s, true, a, p, (const float2*)means);
   });
-  return e != cudaSuccess || !params ? e : param_reduce(a, rows, a.batch * p.splits, s);
+  return e != cudaSuccess ? e : param_reduce(a, a.batch * p.splits, s);
 }
 
 }  // namespace m3

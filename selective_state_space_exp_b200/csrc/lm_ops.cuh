@@ -73,6 +73,8 @@ struct NormArgs {
   void* dz;
   float* dw;
   float* db;
+  float* part_w;   // rows of partial sums of dw and db (or dw and db themselves), or nullptr
+  float* part_b;
   char* ws;
   int* status;
 };

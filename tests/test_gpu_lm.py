@@ -113,6 +113,8 @@ def test_norm_of_tokens(T, G, cg, act, io):
 SEQ = [  # samples, positions, groups, channels of a group
     (1, 1, 1, 8), (2, 2, 3, 5), (3, 7, 2, 16), (2, 129, 5, 24), (4, 300, 3, 31), (1, 1000, 2, 64),
     (2, 65, 1, 2500), (70, 3, 4, 6), (2, 513, 40, 8), (1, 700, 1, 300),
+    # long samples, which several blocks share, and those at the border
+    (2, 3000, 2, 24), (1, 9000, 1, 8), (3, 700, 3, 31), (2, 900, 40, 8), (1, 8192, 1, 8), (1, 8193, 1, 8),
 ]
 
 
@@ -131,12 +133,12 @@ def test_norm_of_sequences(B, L, G, cg, act, io):
     check_norm(x, z, dy, w, b, G, act, spans, y, mean, rstd, g)
 
 
+@pytest.mark.parametrize("cu", [[3, 3, 4, 4, 67, 300, 301], [3, 3, 4, 4, 90, 4800, 4801]])
 @pytest.mark.parametrize("io", ["bf16", "f32"])
-def test_norm_of_a_packed_batch(io):
+def test_norm_of_a_packed_batch(io, cu):
     """Lengths 0, 1 and long ones, rows before the first sequence and behind the last:
     these keep what y held."""
-    cu = [3, 3, 4, 4, 67, 300, 301]
-    T, G, cg = 320, 3, 24
+    T, G, cg = cu[-1] + 19, 3, 24
     for act in ("silu", "gate"):
         x, z, dy, w, b = norm_inputs(T, G * cg, io, act, 5)
         c = torch.tensor(cu, dtype=torch.int32).cuda()
@@ -146,7 +148,7 @@ def test_norm_of_a_packed_batch(io):
         g = m3.m3_group_norm_bwd_varlen(c, d[0], G, mean, rstd, d[2], d[3], d[4], d[1], act=act)
         ok()
         spans = list(zip(cu[:-1], cu[1:]))
-        assert (y[:3] == 7).all() and (y[301:] == 7).all()
+        assert (y[:3] == 7).all() and (y[cu[-1]:] == 7).all()
         assert (mean[0] == 0).all() and (rstd[0] == 0).all()      # an empty sequence
         check_norm(x, z, dy, w, b, G, act, spans, y, mean, rstd, g)
 
