@@ -41,21 +41,22 @@ namespace {
 
 using namespace tc;
 
-constexpr int kBM = 128, kBN = 256, kBK = 64;  // a CTA's rows of a tile, columns, reduction step
+constexpr int kBM = 128, kBK = 64;       // a CTA's rows of a tile, reduction step
+constexpr int kWide = 256, kMiddle = 128, kNarrow = 64;  // columns of a tile
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kBlk = 64 * kBK * 2;  // an MN-major block: 64 columns x 64 reduction rows
-constexpr int kTmemCols = 2 * kBN;
 
 // CG: CTAs that share a tile of CG * 128 rows (a pair's tensor cores work on one
 // tile, each CTA holding its own rows of A and half the columns of B, which
 // halves what the pair reads of B).
-template <int CG>
+template <int CG, int BN>
 struct Cfg {
   static constexpr int A_BYTES = kBM * kBK * 2;
-  static constexpr int B_COLS = kBN / CG;
+  static constexpr int B_COLS = BN / CG;
+  static constexpr int TMEM = 2 * BN;  // columns of two accumulators
   static constexpr int STAGE = A_BYTES + B_COLS * kBK * 2;
-  static constexpr int STAGES = CG == 2 ? 6 : 4;
+  static constexpr int STAGES = BN == kNarrow ? 8 : BN == kMiddle || CG == 2 ? 6 : 4;
   static constexpr int BAR_OFF = STAGES * STAGE;
   static constexpr int SMEM = BAR_OFF + (2 * STAGES + 5) * 8 + 16;
   static_assert(SMEM + 1024 <= 232448, "shared memory");
@@ -70,7 +71,9 @@ enum Mode { kStats = 0, kDlogits = 1, kGrad = 2 };
 struct GemmArgs {
   int64_t M, N;           // extent of the output
   int kb, kb_per;         // reduction blocks in all, and of one split
-  int cg, mt, nt, splits; // CTAs of a tile; tiles
+  int cg, bn;             // CTAs of a tile, its columns
+  int mt, nt, splits;     // tiles
+  int a_rows;             // of A that a stage loads: fewer than kBM where M is smaller
   bool dependent;         // not the call's first kernel
   int* status;
   // stats, dlogits: rows are tokens, columns classes v0 + n
@@ -89,6 +92,8 @@ struct GemmArgs {
   bool add;               // acc holds an earlier sum
 };
 
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 struct Maps {
   CUtensorMap a, b;
 };
@@ -99,16 +104,24 @@ __device__ __forceinline__ unsigned long long now_ns() {
   return t;
 }
 
+// The clock is read now and then only: its value takes longer than most waits.
 __device__ bool wait(uint64_t* bar, uint32_t parity, int* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = now_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (now_ns() - t0 > kWaitNs) {
+  unsigned long long t0 = 0;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if (i % 64 != 0) continue;
+    const unsigned long long t = now_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitNs) {
       if (status) atomicCAS(status, 0, (int)M3_ERR_TIMEOUT);
       return false;
     }
   }
   return true;
+}
+
+// By a whole warp: every lane gets the same answer.
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, int* status) {
+  return __all_sync(0xffffffffu, wait(bar, parity, status));
 }
 
 __device__ __forceinline__ void arrive(uint64_t* bar) {
@@ -165,25 +178,25 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
         : "memory");
   }
 }
-template <int CG>
+template <int CG, int COLS>
 __device__ __forceinline__ void alloc(uint32_t* holder) {
   if constexpr (CG == 1) {
-    tmem_alloc(holder, kTmemCols);
+    tmem_alloc(holder, COLS);
     tmem_relinquish();
   } else {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(holder)),
-                 "r"(kTmemCols)
+                 "r"(COLS)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
 }
-template <int CG>
+template <int CG, int COLS>
 __device__ __forceinline__ void dealloc(uint32_t taddr) {
   if constexpr (CG == 1)
-    tmem_dealloc(taddr, kTmemCols);
+    tmem_dealloc(taddr, COLS);
   else
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(kTmemCols)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(COLS)
                  : "memory");
 }
 __device__ __forceinline__ void pair_sync() {
@@ -249,11 +262,11 @@ __device__ __forceinline__ float largest_dloss(const GemmArgs& g, float* s_max) 
   return c > 0.f && c < INFINITY ? c : 1.f;
 }
 
-template <int MODE>
+template <int MODE, int BN>
 __device__ __forceinline__ void epilogue(const GemmArgs& g, const Tile& t, int64_t row0,
                                          uint32_t tcol, int q, int half, int lane, float unit) {
   const int64_t m = row0 + 32 * q + lane;
-  const int64_t n0 = (int64_t)t.n * kBN + half * (kBN / 2);
+  const int64_t n0 = (int64_t)t.n * BN + half * (BN / 2);
   const bool on = m < g.M;
   if constexpr (MODE == kStats) {
     int64_t tgt = -1;
@@ -261,7 +274,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const Tile& t, int64
     const int64_t rel = tgt - n0;  // the target's column in this half tile
     float mx = -INFINITY, sum = 0.f;
 #pragma unroll 1
-    for (int c = 0; c < kBN / 2; c += 32) {
+    for (int c = 0; c < BN / 2; c += 32) {
       uint32_t v[32];
       tmem_ld32(tcol + (uint32_t)c, v);
       tmem_ld_wait();
@@ -304,7 +317,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const Tile& t, int64
     }
     const int64_t rel = tgt - g.v0 - n0;
 #pragma unroll 1
-    for (int c = 0; c < kBN / 2; c += 32) {
+    for (int c = 0; c < BN / 2; c += 32) {
       uint32_t v[32];
       tmem_ld32(tcol + (uint32_t)c, v);
       tmem_ld_wait();
@@ -328,7 +341,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const Tile& t, int64
     float* acc = g.acc ? g.acc + ((int64_t)t.split * g.M + m) * g.N + n0 : nullptr;
     __nv_bfloat16* out = g.out ? g.out + m * g.N + n0 : nullptr;
 #pragma unroll 1
-    for (int c = 0; c < kBN / 2; c += 32) {
+    for (int c = 0; c < BN / 2; c += 32) {
       uint32_t v[32];
       tmem_ld32(tcol + (uint32_t)c, v);
       tmem_ld_wait();
@@ -360,15 +373,15 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const Tile& t, int64
   }
 }
 
-template <int CG, int MODE, bool AMN, bool BMN>
+template <int CG, int BN, int MODE, bool AMN, bool BMN>
 __global__ void __launch_bounds__(kThreads, 1)
 xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
-  using C = Cfg<CG>;
+  using C = Cfg<CG, BN>;
   constexpr int kStages = C::STAGES;
   let_next_start();
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sbase = smem_u32(sm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if ((sbase & 1023u) != 0) {  // the swizzled layout needs 1 KB alignment
     if (tid == 0 && g.status) atomicCAS(g.status, 0, (int)M3_ERR_CUDA);
     return;
@@ -399,62 +412,80 @@ xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
     __syncthreads();
     pair_sync();  // the other CTA's barriers are ready
   }
-  if (warp == 1) alloc<CG>(s_tmem);
+  if (warp == 1) alloc<CG, C::TMEM>(s_tmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = *s_tmem;
   wait_for_previous();
 
-  if (warp == 0 && lane == 0) {
-    uint32_t it = 0;
+  if (warp == 0) {
+    const uint32_t bytes = (uint32_t)(CG * (g.a_rows * kBK * 2 + C::B_COLS * kBK * 2));
+    uint32_t s = 0, phase = 0;
+    int64_t loads = 0;
     bool ok = true;
     for (int64_t t = first; t < tiles && ok; t += step) {
       const Tile tl = tile_of<CG>(g, t);
       const int k0 = tl.split * g.kb_per, k1 = k0 + g.kb_per < g.kb ? k0 + g.kb_per : g.kb;
-      for (int kb = k0; kb < k1; ++kb, ++it) {
-        const int s = (int)(it % kStages);
-        if (!wait(&empty[s], ((it / kStages) & 1u) ^ 1u, g.status)) { ok = false; break; }
-        uint8_t* st = sm + s * C::STAGE;
-        const uint32_t bar = CG == 2 ? in_first_cta(&full[s]) : 0;
-        if (rank == 0) mbar_expect_tx(&full[s], (uint32_t)(CG * C::STAGE));
-        load_operand<CG, AMN, kBM>(st, &maps.a, (tl.m * CG + rank) * kBM, kb * kBK, &full[s], bar);
-        load_operand<CG, BMN, C::B_COLS>(st + C::A_BYTES, &maps.b, tl.n * kBN + rank * C::B_COLS,
-                                         kb * kBK, &full[s], bar);
+      const int arow = (tl.m * CG + rank) * kBM, brow = tl.n * BN + rank * C::B_COLS;
+      for (int kb = k0; kb < k1; ++kb, ++loads) {
+        if (!wait_all(&empty[s], phase ^ 1u, g.status)) { ok = false; break; }
+        if (elect_one()) {
+          uint8_t* st = sm + s * C::STAGE;
+          const uint32_t bar = CG == 2 ? in_first_cta(&full[s]) : 0;
+          if (rank == 0) mbar_expect_tx(&full[s], bytes);
+          load_operand<CG, AMN, kBM>(st, &maps.a, arow, kb * kBK, &full[s], bar);
+          load_operand<CG, BMN, C::B_COLS>(st + C::A_BYTES, &maps.b, brow, kb * kBK, &full[s], bar);
+        }
+        __syncwarp();
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1u;
+        }
       }
     }
     // let the last stages' copies land (bounded) before the CTA can exit: the
     // first CTA's barriers see both CTAs' copies, the other CTA waits for the
     // MMAs that have read its own
-    for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-      wait(rank == 0 ? &full[j % kStages] : &empty[j % kStages], (j / kStages) & 1u, g.status);
-  } else if (warp == 1 && lane == 0 && rank == 0) {
-    const uint32_t idesc = idesc_bf16(CG * kBM, kBN, AMN, BMN);
-    uint32_t it = 0;
+    for (int64_t j = loads > kStages ? loads - kStages : 0; j < loads; ++j)
+      wait(rank == 0 ? &full[j % kStages] : &empty[j % kStages], (uint32_t)(j / kStages) & 1u, g.status);
+  } else if (warp == 1 && rank == 0) {
+    // the whole warp keeps step and one lane issues: descriptors then live in
+    // uniform registers, where a single lane's branch would move each operand of
+    // each instruction there (a step of four MMAs: about 120 cycles against 283)
+    constexpr uint32_t idesc = idesc_bf16(CG * kBM, BN, AMN, BMN);
+    // K-major: 16 reduction columns are 32 bytes on; MN-major: 16 rows of 128 bytes
+    const uint64_t a0 = sw128_desc(sbase, AMN ? kBlk : 16, 1024);
+    const uint64_t b0 = sw128_desc(sbase + C::A_BYTES, BMN ? kBlk : 16, 1024);
+    uint32_t s = 0, phase = 0;
     int j = 0;
     bool ok = true;
     for (int64_t t = first; t < tiles && ok; t += step, ++j) {
       const Tile tl = tile_of<CG>(g, t);
       const int k0 = tl.split * g.kb_per, k1 = k0 + g.kb_per < g.kb ? k0 + g.kb_per : g.kb;
       const int b = j & 1;
-      if (!wait(&acc_empty[b], ((j >> 1) & 1) ^ 1u, g.status)) break;
+      if (!wait_all(&acc_empty[b], ((j >> 1) & 1) ^ 1u, g.status)) break;
       tc_fence_after();
-      const uint32_t dcol = tm + (uint32_t)(b * kBN);
-      for (int kb = k0; kb < k1; ++kb, ++it) {
-        const int s = (int)(it % kStages);
-        if (!wait(&full[s], (it / kStages) & 1u, g.status)) { ok = false; break; }
+      const uint32_t dcol = tm + (uint32_t)(b * BN);
+      for (int kb = k0; kb < k1; ++kb) {
+        if (!wait_all(&full[s], phase, g.status)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t st = sbase + (uint32_t)(s * C::STAGE);
-        // K-major: 16 reduction columns are 32 bytes on; MN-major: 16 rows of 128 bytes
-        const uint64_t ad = sw128_desc(st, AMN ? kBlk : 16, 1024);
-        const uint64_t bd = sw128_desc(st + C::A_BYTES, BMN ? kBlk : 16, 1024);
+        const uint64_t ad = a0 + s * (C::STAGE >> 4), bd = b0 + s * (C::STAGE >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int k4 = 0; k4 < kBK / 16; ++k4)
-          mma<CG>(dcol, ad + (uint64_t)(k4 * (AMN ? 128 : 2)),
-                  bd + (uint64_t)(k4 * (BMN ? 128 : 2)), idesc, kb > k0 || k4 > 0);
-        commit<CG>(&empty[s]);
+          for (int k4 = 0; k4 < kBK / 16; ++k4)
+            mma<CG>(dcol, ad + (uint64_t)(k4 * (AMN ? 128 : 2)),
+                    bd + (uint64_t)(k4 * (BMN ? 128 : 2)), idesc, kb > k0 || k4 > 0);
+          commit<CG>(&empty[s]);
+        }
+        __syncwarp();
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1u;
+        }
       }
-      if (ok) commit<CG>(&acc_full[b]);
+      if (ok && elect_one()) commit<CG>(&acc_full[b]);
+      __syncwarp();
     }
   } else if (warp >= 2) {
     const int q = warp & 3;  // TMEM lane quadrant this warp may access
@@ -469,11 +500,11 @@ xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
     int j = 0;
     for (int64_t t = first; t < tiles; t += step, ++j) {
       const int b = j & 1;
-      if (!__all_sync(0xffffffffu, wait(&acc_full[b], (j >> 1) & 1u, g.status))) break;
+      if (!wait_all(&acc_full[b], (j >> 1) & 1u, g.status)) break;
       tc_fence_after();
       const Tile tl = tile_of<CG>(g, t);
-      epilogue<MODE>(g, tl, (int64_t)(tl.m * CG + rank) * kBM,
-                     tm + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * kBN + half * (kBN / 2)), q,
+      epilogue<MODE, BN>(g, tl, (int64_t)(tl.m * CG + rank) * kBM,
+                     tm + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * BN + half * (BN / 2)), q,
                      half, lane, unit);
       tc_fence_before();
       __syncwarp();
@@ -488,13 +519,14 @@ xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1 && lane == 0 && rank == 0) {
-    commit<CG>(s_fin);
+  if (warp == 1 && rank == 0) {
+    if (elect_one()) commit<CG>(s_fin);
+    __syncwarp();
     wait(s_fin, 0, g.status);
   }
   __syncwarp();
   if (CG == 2) pair_sync();
-  if (warp == 1) dealloc<CG>(tm);
+  if (warp == 1) dealloc<CG, C::TMEM>(tm);
 }
 
 // (maximum, sum) of the exponentials of two sets.
@@ -545,21 +577,42 @@ xent_join_kernel(const float2* stat, int parts, int64_t M, int64_t V, const int6
   }
 }
 
-// out = c times the sum over splits of part[s], rounded to bf16; n is a multiple of 8.
+// out = c times the sum over splits of part[s], rounded to bf16; n is a multiple of
+// 8.  LANES threads share the splits of four neighbouring sums.
+template <int LANES>
 __global__ void __launch_bounds__(256)
 xent_sum_kernel(const float* part, int splits, int64_t n, const float* unit, __nv_bfloat16* out) {
+  constexpr int kCols = 256 / LANES;
   let_next_start();
   wait_for_previous();
+  __shared__ float4 s_part[LANES][kCols];
+  const int x = threadIdx.x % kCols, y = threadIdx.x / kCols;
   const float c = *unit;
-  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n;
-       i += (int64_t)gridDim.x * 1024) {
-    float4 f = *reinterpret_cast<const float4*>(part + i);
-    for (int s = 1; s < splits; ++s) {
-      const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)s * n + i);
-      f.x += v.x; f.y += v.y; f.z += v.z; f.w += v.w;
+  for (int64_t i0 = (int64_t)blockIdx.x * kCols * 4; i0 < n; i0 += (int64_t)gridDim.x * kCols * 4) {
+    const int64_t i = i0 + x * 4;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < n) {
+#pragma unroll 4
+      for (int s = y; s < splits; s += LANES) {
+        const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)s * n + i);
+        f.x += v.x; f.y += v.y; f.z += v.z; f.w += v.w;
+      }
     }
-    *reinterpret_cast<uint2*>(out + i) = 
-        make_uint2(pack_bf16(f.x * c, f.y * c), pack_bf16(f.z * c, f.w * c));
+    if constexpr (LANES > 1) {
+      s_part[y][x] = f;
+      __syncthreads();
+      if (y == 0) {
+#pragma unroll
+        for (int l = 1; l < LANES; ++l) {
+          const float4 v = s_part[l][x];
+          f.x += v.x; f.y += v.y; f.z += v.z; f.w += v.w;
+        }
+      }
+      __syncthreads();
+    }
+    if (y == 0 && i < n)
+      *reinterpret_cast<uint2*>(out + i) =
+          make_uint2(pack_bf16(f.x * c, f.y * c), pack_bf16(f.z * c, f.w * c));
   }
 }
 
@@ -602,15 +655,19 @@ struct Operand {
   int64_t rows, cols, ld;
 };
 
-template <int CG, int MODE, bool AMN, bool BMN>
-cudaError_t gemm_cg(const GemmArgs& g, const Operand& a, const Operand& b, cudaStream_t s) {
-  using C = Cfg<CG>;
+template <int CG, int BN, int MODE, bool AMN, bool BMN>
+cudaError_t gemm_cg(const GemmArgs& g0, const Operand& a, const Operand& b, cudaStream_t s) {
+  using C = Cfg<CG, BN>;
+  // the rows of a stage behind A's last keep what shared memory held: they give
+  // rows of the output that are not stored
+  GemmArgs g = g0;
+  g.a_rows = !AMN && g.M < kBM ? (int)ceil_div(g.M, 8) * 8 : kBM;
   Maps maps;
   memset(&maps, 0, sizeof(maps));
-  if (!encode(&maps.a, a.p, a.rows, a.cols, a.ld, AMN ? kBK : kBM) ||
+  if (!encode(&maps.a, a.p, a.rows, a.cols, a.ld, AMN ? kBK : g.a_rows) ||
       !encode(&maps.b, b.p, b.rows, b.cols, b.ld, BMN ? kBK : C::B_COLS))
     return cudaErrorInvalidValue;
-  auto kern = xent_gemm_kernel<CG, MODE, AMN, BMN>;
+  auto kern = xent_gemm_kernel<CG, BN, MODE, AMN, BMN>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
@@ -624,31 +681,56 @@ cudaError_t gemm_cg(const GemmArgs& g, const Operand& a, const Operand& b, cudaS
 
 template <int MODE, bool AMN, bool BMN>
 cudaError_t gemm(const GemmArgs& g, const Operand& a, const Operand& b, cudaStream_t s) {
-  return g.cg == 2 ? gemm_cg<2, MODE, AMN, BMN>(g, a, b, s) : gemm_cg<1, MODE, AMN, BMN>(g, a, b, s);
+  if (g.cg == 2) return gemm_cg<2, kWide, MODE, AMN, BMN>(g, a, b, s);
+  if (g.bn == kNarrow) return gemm_cg<1, kNarrow, MODE, AMN, BMN>(g, a, b, s);
+  if (g.bn == kMiddle) return gemm_cg<1, kMiddle, MODE, AMN, BMN>(g, a, b, s);
+  return gemm_cg<1, kWide, MODE, AMN, BMN>(g, a, b, s);
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// How a product's output is cut.
+struct Cut {
+  int cg, bn, splits;
+};
 
-void set_tiles(GemmArgs* g, int64_t M, int64_t N, int64_t K, int splits) {
+// A product with M x N outputs, reduced over K in steps of 64.  Pairs of CTAs on
+// 256 x 256 tiles where these fill three quarters of the SMs or more; else single
+// ones, with the columns and the splits of the reduction for which the longest
+// CTA loads least (24, 32 or 48 KB a step; a step's time goes with that: 0.16 to
+// 0.42 us).  Splits are at least eight steps long, and the launch that adds them
+// counts as sixteen narrow steps.  Measured: 77 x 1003 classes x 256, the four
+// products of a loss with gradients, 21 us with narrow tiles against 32 us with
+// wide ones; logits of 28 x 10776 x 1744 15.4 us (middle) against 19.2 (wide); but
+// dh of 391 x 56104 x 3296 181 us (wide, two splits) against 280 (middle).
+Cut cut_of(int64_t M, int64_t N, int64_t K, bool split) {
+  if (ceil_div(M, 2 * kBM) * ceil_div(N, kWide) >= kPlanSms / 2 * 3 / 4) return Cut{2, kWide, 1};
+  const int64_t mt = ceil_div(M, kBM), kb = ceil_div(K, kBK);
+  Cut best{1, kWide, 1};
+  int64_t least = INT64_MAX;
+  for (int bn : {kWide, kMiddle, kNarrow}) {
+    const int64_t tiles = mt * ceil_div(N, bn);
+    int64_t s = split ? kPlanSms / tiles : 1;
+    if (s > kb / 8) s = kb / 8;
+    if (s < 1) s = 1;
+    s = ceil_div(kb, ceil_div(kb, s));
+    const int64_t loads = ceil_div(tiles * s, kPlanSms) * ceil_div(kb, s) * (kBM + bn) / 8 + (s > 1 ? 16 * 24 : 0);
+    if (loads < least) {
+      least = loads;
+      best = Cut{1, bn, (int)s};
+    }
+  }
+  return best;
+}
+
+void set_tiles(GemmArgs* g, int64_t M, int64_t N, int64_t K, const Cut& c) {
   g->M = M;
   g->N = N;
-  // pairs of CTAs where their larger tiles still fill most SMs
-  const int64_t pairs = ceil_div(M, 2 * kBM) * ceil_div(N, kBN);
-  g->cg = splits == 1 && pairs >= kPlanSms / 2 * 3 / 4 ? 2 : 1;
-  g->mt = (int)ceil_div(M, g->cg * kBM);
-  g->nt = (int)ceil_div(N, kBN);
+  g->cg = c.cg;
+  g->bn = c.bn;
+  g->mt = (int)ceil_div(M, c.cg * kBM);
+  g->nt = (int)ceil_div(N, c.bn);
   g->kb = (int)ceil_div(K, kBK);
-  g->kb_per = (int)ceil_div(g->kb, splits);
+  g->kb_per = (int)ceil_div(g->kb, c.splits);
   g->splits = (int)ceil_div(g->kb, g->kb_per);
-}
-
-// Splits of a reduction of `kb` blocks over `tiles` output tiles: as many as
-// keep every SM busy, each at least four blocks long.
-int splits_for(int64_t tiles, int64_t kb) {
-  int64_t s = kPlanSms / tiles;
-  if (s > kb / 4) s = kb / 4;
-  if (s < 1) s = 1;
-  return (int)ceil_div(kb, ceil_div(kb, s));
 }
 
 // Bytes that the workspace may hold of d at a time: large enough that the
@@ -657,38 +739,41 @@ constexpr int64_t kPieceBytes = (int64_t)256 << 20;
 
 struct BwdPlan {
   int64_t piece, ldd;  // classes of one piece, and its row length (a multiple of 64)
-  int pieces, dh_splits, dw_splits;
+  int pieces;
+  Cut dh, dw;
   size_t d_bytes, dh_bytes, dw_bytes;
 };
 
 BwdPlan bwd_plan(const XentArgs& a) {
   BwdPlan p;
-  int64_t most = kPieceBytes / 2 / a.M / kBN * kBN;
-  if (most < kBN) most = kBN;
+  int64_t most = kPieceBytes / 2 / a.M / kWide * kWide;
+  if (most < kWide) most = kWide;
   p.pieces = (int)ceil_div(a.V, most);
-  p.piece = ceil_div(ceil_div(a.V, p.pieces), kBN) * kBN;
+  p.piece = ceil_div(ceil_div(a.V, p.pieces), kWide) * kWide;
   p.pieces = (int)ceil_div(a.V, p.piece);
   if (p.pieces == 1) p.piece = a.V;
   p.ldd = ceil_div(p.piece, 64) * 64;
-  const int64_t kt = ceil_div(a.K, kBN);
-  p.dh_splits = splits_for(ceil_div(a.M, kBM) * kt, ceil_div(p.piece, kBK));
-  p.dw_splits = splits_for(ceil_div(p.piece, kBM) * kt, ceil_div(a.M, kBK));
+  p.dh = cut_of(a.M, a.K, p.piece, true);
+  p.dw = cut_of(p.piece, a.K, a.M, true);
   p.d_bytes = align_up((size_t)a.M * p.ldd * 2, 256);
-  p.dh_bytes = p.pieces > 1 || p.dh_splits > 1
-                   ? align_up((size_t)p.dh_splits * a.M * a.K * 4, 256) : 0;
-  p.dw_bytes = p.dw_splits > 1 ? align_up((size_t)p.dw_splits * p.piece * a.K * 4, 256) : 0;
+  p.dh_bytes = p.pieces > 1 || p.dh.splits > 1
+                   ? align_up((size_t)p.dh.splits * a.M * a.K * 4, 256) : 0;
+  p.dw_bytes = p.dw.splits > 1 ? align_up((size_t)p.dw.splits * p.piece * a.K * 4, 256) : 0;
   return p;
 }
 
 size_t fwd_stat_bytes(const XentArgs& a) {
-  return align_up((size_t)2 * ceil_div(a.V, kBN) * a.M * sizeof(float2), 256);
+  return align_up((size_t)2 * ceil_div(a.V, cut_of(a.M, a.V, a.K, false).bn) * a.M * sizeof(float2), 256);
 }
 
 cudaError_t sum_splits(const float* part, int splits, int64_t n, const float* unit, void* out,
                        cudaStream_t s) {
-  const int64_t blocks = ceil_div(n, 1024);
-  return launch_kernel(xent_sum_kernel, dim3((unsigned)(blocks < kPlanSms * 8 ? blocks : kPlanSms * 8)),
-                       256, 0, s, true, 1, part, splits, n, unit, static_cast<__nv_bfloat16*>(out));
+  // few sums: eight threads each
+  const bool few = n < (int64_t)kPlanSms * 1024 && splits >= 8;
+  const int64_t blocks = ceil_div(n, few ? 128 : 1024);
+  return launch_kernel(few ? xent_sum_kernel<8> : xent_sum_kernel<1>,
+                       dim3((unsigned)(blocks < kPlanSms * 8 ? blocks : kPlanSms * 8)), 256, 0, s, true, 1,
+                       part, splits, n, unit, static_cast<__nv_bfloat16*>(out));
 }
 
 }  // namespace
@@ -703,7 +788,7 @@ size_t xent_workspace(const XentArgs& a, bool backward) {
 cudaError_t xent_fwd_launch(const XentArgs& a, cudaStream_t s) {
   GemmArgs g;
   memset(&g, 0, sizeof(g));
-  set_tiles(&g, a.M, a.V, a.K, 1);
+  set_tiles(&g, a.M, a.V, a.K, cut_of(a.M, a.V, a.K, false));
   g.status = a.status;
   g.targets = a.targets;
   g.ignore = a.ignore;
@@ -729,7 +814,7 @@ cudaError_t xent_bwd_launch(const XentArgs& a, cudaStream_t s) {
     const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.W) + v0 * a.K;
     GemmArgs g;
     memset(&g, 0, sizeof(g));
-    set_tiles(&g, a.M, n, a.K, 1);
+    set_tiles(&g, a.M, n, a.K, cut_of(a.M, n, a.K, false));
     g.dependent = i > 0;
     g.status = a.status;
     g.targets = a.targets;
@@ -747,7 +832,7 @@ cudaError_t xent_bwd_launch(const XentArgs& a, cudaStream_t s) {
     if (a.dW) {  // [n][K] = d^T h
       GemmArgs w;
       memset(&w, 0, sizeof(w));
-      set_tiles(&w, n, a.K, a.M, p.dw_splits);
+      set_tiles(&w, n, a.K, a.M, p.dw);
       w.dependent = true;
       w.status = a.status;
       w.unit = unit;
@@ -760,17 +845,17 @@ cudaError_t xent_bwd_launch(const XentArgs& a, cudaStream_t s) {
     if (a.dh) {  // [M][K] += d W
       GemmArgs h;
       memset(&h, 0, sizeof(h));
-      set_tiles(&h, a.M, a.K, n, p.dh_splits);
+      set_tiles(&h, a.M, a.K, n, p.dh);
       h.dependent = true;
       h.status = a.status;
       h.unit = unit;
       const bool last = i + 1 == p.pieces;
       h.add = i > 0;
       if (p.dh_bytes) h.acc = dh32;
-      if (last && p.dh_splits == 1) h.out = static_cast<__nv_bfloat16*>(a.dh);
+      if (last && p.dh.splits == 1) h.out = static_cast<__nv_bfloat16*>(a.dh);
       e = gemm<kGrad, false, true>(h, Operand{d, a.M, n, p.ldd}, Operand{W, n, a.K, a.K}, s);
-      if (e == cudaSuccess && last && p.dh_splits > 1)
-        e = sum_splits(dh32, p.dh_splits, a.M * a.K, unit, a.dh, s);
+      if (e == cudaSuccess && last && p.dh.splits > 1)
+        e = sum_splits(dh32, p.dh.splits, a.M * a.K, unit, a.dh, s);
       if (e != cudaSuccess) return e;
     }
   }

@@ -23,6 +23,17 @@ __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(on));
+  return on != 0;
+}
+
 // Launches a kernel; dependent: as a programmatic dependent of the kernel before
 // it in the stream (one of the same call); cluster: blocks of a cluster along x.
 template <typename... P, typename... A>
