@@ -96,6 +96,11 @@ __device__ __forceinline__ bool w4_wait(uint64_t* bar, uint32_t parity, int* sta
   }
 }
 
+// By a whole warp: every lane gets the same answer.
+__device__ __forceinline__ bool w4_wait_all(uint64_t* bar, uint32_t parity, int* status) {
+  return __all_sync(0xffffffffu, w4_wait(bar, parity, status));
+}
+
 // Input of word w (0..3) of lane column c (0..3) in a chunk of 128: per group a
 // lane has group / 4 consecutive inputs, eight a word.
 template <int G>
@@ -690,7 +695,7 @@ w4_tc_kernel(const W4Args a, const TcPlan p, const __grid_constant__ CUtensorMap
   constexpr int NG = kStep / G;             // groups of a step
   constexpr int CB = kBlock / NG;           // steps of a block of scales
   extern __shared__ __align__(1024) uint8_t sm[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if ((smem_u32(sm) & 1023u) != 0) {
     if (threadIdx.x == 0 && a.status) atomicCAS(a.status, 0, (int)M3_ERR_CUDA);
     return;
@@ -920,26 +925,32 @@ w4_tc_kernel(const W4Args a, const TcPlan p, const __grid_constant__ CUtensorMap
         bar_arrive(&p_full[slot]);
       }
     }
-  } else if (warp == 2 * kWorkers && lane == 0) {
+  } else if (warp == 2 * kWorkers) {
     // ---- TMA ------------------------------------------------------------------------
     Turn code, xt;
     uint32_t nx = 0, ncode = 0;
     for (int tile = tile0; tile < p.tiles && ok; tile += tstep) {
       for (int c = 0; c < nc && ok; ++c) {
-        ok = w4_wait(&c_empty[code.slot], code.phase ^ 1u, a.status);
+        ok = w4_wait_all(&c_empty[code.slot], code.phase ^ 1u, a.status);
         if (!ok) break;
-        mbar_expect_tx(&c_full[code.slot], kCodeBox);
-        tma_box(sm + code.slot * kCodeBox, &cmap, (c0 + c) * (kStep / 2), tile * kTileRows,
-                &c_full[code.slot]);
+        if (elect_one()) {
+          mbar_expect_tx(&c_full[code.slot], kCodeBox);
+          tma_box(sm + code.slot * kCodeBox, &cmap, (c0 + c) * (kStep / 2), tile * kTileRows,
+                  &c_full[code.slot]);
+        }
+        __syncwarp();
         code.next(Cf::CBUFS);
         ++ncode;
-        ok = w4_wait(&s_done[xt.slot], xt.phase ^ 1u, a.status);
+        ok = w4_wait_all(&s_done[xt.slot], xt.phase ^ 1u, a.status);
         if (!ok) break;
-        mbar_expect_tx(&x_full[xt.slot], Cf::XBYTES);
-        uint8_t* xs = sm + Cf::X_OFF + xt.slot * Cf::XBYTES;
+        if (elect_one()) {
+          mbar_expect_tx(&x_full[xt.slot], Cf::XBYTES);
+          uint8_t* xs = sm + Cf::X_OFF + xt.slot * Cf::XBYTES;
 #pragma unroll
-        for (int i = 0; i < kStep / 64; ++i)
-          tma_box(xs + i * NTOK * 128, &xmap, (c0 + c) * kStep + i * 64, m0, &x_full[xt.slot]);
+          for (int i = 0; i < kStep / 64; ++i)
+            tma_box(xs + i * NTOK * 128, &xmap, (c0 + c) * kStep + i * 64, m0, &x_full[xt.slot]);
+        }
+        __syncwarp();
         xt.next(Cf::XBUFS);
         ++nx;
       }
@@ -950,8 +961,10 @@ w4_tc_kernel(const W4Args a, const TcPlan p, const __grid_constant__ CUtensorMap
     for (uint32_t k = nx > Cf::XBUFS ? nx - Cf::XBUFS : 0; k < nx; ++k)
       w4_wait(&x_full[k % Cf::XBUFS], (k / Cf::XBUFS) & 1u, a.status);
   } else if (warp == 2 * kWorkers + 1) {
-    // ---- MMA issue: the sums of a set in turn, so that none waits on the last ---------
-    const uint32_t idesc = idesc_bf16(kTileRows, NTOK, 0, 0);
+    // ---- MMA issue: the sums of a set in turn, so that none waits on the last; the
+    // whole warp keeps step and one lane issues (descriptors in uniform registers) -------
+    constexpr uint32_t idesc = idesc_bf16(kTileRows, NTOK, 0, 0);
+    const uint64_t x0 = sw128_desc(smem_u32(sm) + Cf::X_OFF, 16, 1024);
     Turn at, xt, dt;
     for (int tile = tile0; tile < p.tiles && ok; tile += tstep) {
       for (int c = 0; c < nc && ok; ++c) {
@@ -960,15 +973,14 @@ w4_tc_kernel(const W4Args a, const TcPlan p, const __grid_constant__ CUtensorMap
         const uint32_t ph = lane == 0 ? xt.phase : lane == 1 ? at.phase : dt.phase ^ 1u;
         if (lane < 3) ok = w4_wait(bar, ph, a.status);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint64_t xd = sw128_desc(smem_u32(sm) + Cf::X_OFF + xt.slot * Cf::XBYTES, 16, 1024);
+        const uint64_t xd = x0 + xt.slot * (Cf::XBYTES >> 4);
         const uint32_t acol = tm + at.slot * kACols;
-        if (lane == 0) {
 #pragma unroll
-          for (int g = 0; g < Cf::SETS; ++g) {
-            if (g > 0) ok = w4_wait(&d_empty[dt.slot], dt.phase ^ 1u, a.status);
-            if (!ok) break;
-            tc_fence_after();
+        for (int g = 0; g < Cf::SETS; ++g) {
+          if (g > 0) ok = w4_wait_all(&d_empty[dt.slot], dt.phase ^ 1u, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < Cf::SUB / 16; ++k) {
 #pragma unroll
@@ -979,13 +991,11 @@ w4_tc_kernel(const W4Args a, const TcPlan p, const __grid_constant__ CUtensorMap
               }
             }
             mma_commit(&d_full[dt.slot]);
-            dt.next(Cf::DBUFS);
+            if (g == Cf::SETS - 1) mma_commit(&s_done[xt.slot]);
           }
-          if (ok) mma_commit(&s_done[xt.slot]);
+          __syncwarp();
+          dt.next(Cf::DBUFS);
         }
-        ok = __all_sync(0xffffffffu, ok);
-        dt.slot = __shfl_sync(0xffffffffu, dt.slot, 0);
-        dt.phase = __shfl_sync(0xffffffffu, dt.phase, 0);
         at.next(kABufs);
         xt.next(Cf::XBUFS);
       }
@@ -997,10 +1007,9 @@ w4_tc_kernel(const W4Args a, const TcPlan p, const __grid_constant__ CUtensorMap
   __syncthreads();
   tc_fence_after();
   if (warp == 2 * kWorkers + 1) {
-    if (lane == 0) {
-      mma_commit(s_fin);
-      w4_wait(s_fin, 0, a.status);
-    }
+    if (elect_one()) mma_commit(s_fin);
+    __syncwarp();
+    w4_wait(s_fin, 0, a.status);
     __syncwarp();
     tmem_dealloc(tm, 512);
   }
