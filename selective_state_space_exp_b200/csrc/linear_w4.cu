@@ -1108,14 +1108,25 @@ cudaError_t launch_tc(const W4Args& a, cudaStream_t s) {
 }
 
 // Up to 16 tokens the mma.sync form: the tcgen05 one pays the same for any few
-// tokens (50257 x 2048, groups of 128, one token: 27.0 us against 17.3 us; 16
-// tokens: 27.6 against 24.7; 32 tokens: 30 against 47).
+// tokens (50257 x 2048, groups of 128, one token: 22 us against 17.3; 16 tokens:
+// 25.6 against 25.0; 32 tokens: 25.7 against 47).
+//
+// Above 64 tokens, tiles of 128 or several of 64, which decode the weights again.
+// Tiles of 64 where groups are of 32 (their sums wait for TMEM columns, of which 128
+// tokens leave two sets: 128 x 8192 x 4096 28.3 us against 34.9), or where even with
+// them the SMs are not filled twice (300 x 500 x 1024 8.9 us against 13.5).  Else
+// tiles of 128 (512 x 8192 x 4096, groups of 128, 55 us against 79; of 64, 67
+// against 83).
 template <int G, bool ZEROS>
 cudaError_t launch_m(const W4Args& a, cudaStream_t s) {
   if (a.M <= 16) return launch_z<G, ZEROS>(a, s);
   if (a.M <= 32) return launch_tc<G, ZEROS, 32>(a, s);
   if (a.M <= 64) return launch_tc<G, ZEROS, 64>(a, s);
-  return launch_tc<G, ZEROS, 128>(a, s);
+  if constexpr (G > 32) {
+    const int64_t tiles = ((a.N + kTileRows - 1) / kTileRows) * ((a.M + 63) / 64);
+    if (2 * tiles > kPlanSms) return launch_tc<G, ZEROS, 128>(a, s);
+  }
+  return launch_tc<G, ZEROS, 64>(a, s);
 }
 
 template <int G>

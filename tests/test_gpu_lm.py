@@ -268,7 +268,10 @@ def check_xent(h, W, t, dl, loss, lse, dh, dW, ignore=-100):
 
 
 XENT = [(1, 1, 8), (1, 2, 8), (3, 7, 64), (1, 1000, 128), (77, 1003, 256), (128, 256, 64), (129, 257, 72),
-        (300, 5, 200), (1000, 130, 40), (513, 4097, 96), (64, 20000, 64), (200, 515, 1032)]
+        (300, 5, 200), (1000, 130, 40), (513, 4097, 96), (64, 20000, 64), (200, 515, 1032),
+        # other cuts of the products: columns of a tile, pairs, splits
+        (70, 11000, 136), (40, 9000, 1040), (2000, 120, 1000), (1300, 1900, 200), (246, 2376, 536),
+        (260, 9000, 1496)]
 
 
 @pytest.mark.parametrize("M,V,K", XENT)
@@ -427,6 +430,7 @@ W4 = [  # tokens, outputs, inputs, group
     (9, 40, 2048, 32), (16, 130, 1152, 128), (16, 7, 4160, 64), (17, 129, 256, 64), (32, 50, 96, 32),
     (33, 300, 2176, 128), (64, 128, 1024, 32), (65, 257, 512, 128), (128, 64, 4096, 64), (130, 70, 320, 32),
     (300, 33, 640, 128), (5, 4100, 384, 128), (1, 20, 20480, 128), (3, 2, 33280, 64),
+    (65, 4800, 512, 128), (200, 3300, 384, 64), (129, 3200, 256, 32),
 ]
 
 
