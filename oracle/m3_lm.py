@@ -32,10 +32,6 @@ def sigmoid(v):
     return 1.0 / (1.0 + np.exp(-v))
 
 
-def _spans(batch_rows, rows):
-    return [(int(a), int(b)) for a, b in zip(batch_rows[:-1], batch_rows[1:]) if b <= rows]
-
-
 def group_norm(x, groups, w=None, b=None, z=None, act="none", eps=1e-5, spans=None, dy=None):
     """x [T][C] and the samples as (first, end) row pairs (None: every row its
     own).  Returns {"y", "mean", "rstd"} and, given dy, {"x", "w", "b", "z"}.

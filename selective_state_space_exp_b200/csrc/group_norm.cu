@@ -25,12 +25,18 @@
 //                  time reads neighbouring memory.  (Slices held in the shared
 //                  memory of clusters, read once, measured slower: 56 against
 //                  54 us forward and 169 against 100 us backward at 8 x 2048 x
-//                  2048, for the clusters leave SMs idle between them.)
+//                  2048, for the clusters leave SMs idle between them.)  Short
+//                  samples: one block makes both passes.
+// Measured in bf16: 16384 tokens x 4096 channels, 64 groups, with the gate 77 us
+// forward (5.2 TB/s) and 129 us backward (5.2 TB/s, 6 us of it the sums of dw and db);
+// 8 sequences x 2048 x 2048, 32 groups, SiLU 46 us forward and 86 us backward (each
+// of their four passes at 4.5 to 5 TB/s, two joining launches at about 5 us).
 // Statistics are fp32: in the unit kernels the mean first, then the deviations
 // from it (whose own mean corrects it) and their squares; in the others sums about
 // one of the values, merged pairwise as counts, means and squared deviations (Chan,
-// Golub and LeVeque): a large common offset is not squared.  No atomics: dw and db are partial sums in the workspace, added
-// in a fixed order.
+// Golub and LeVeque): a large common offset is not squared.  No atomics: dw and db are
+// partial sums in the workspace, added in a fixed order.  y, dx and dz are rounded to
+// the io type once, at their store.
 #include <type_traits>
 
 #include "lm_ops.cuh"

@@ -19,6 +19,19 @@
 // the low mantissa bits of 128 (0x4300), which makes the number 128 + q, and
 // 128 + z is taken off, both exactly.  The warps' parts of the inputs are added
 // in shared memory in a fixed order.
+//
+// From 17 tokens on the products are tcgen05's: eight warps write the decoded
+// weights to TMEM as the A operand, the tokens' values come by TMA as B, eight more
+// warps add the groups' sums with their scales out of TMEM.
+//
+// Rounding: sums, scales' products and bias in fp32, out rounded once.
+//
+// Measured: one token, 50257 x 2048: 17.3 us (groups of 128), 20.4 us (of 32, zero
+// points): 3.0 TB/s of codes and scales.  What bounds it is taking the codes apart: a
+// word of eight takes three shifts, four masks and four subtractions, 230 instructions
+// in all for 16 x 128 codes, and issue slots are half used.  11 tokens 24.9 us, 32 tokens 25.7, 64 tokens 31.8, 128 tokens x 8192 x 4096 19.8 us: there the
+// decoding, the products and the sums of a step wait on one another.  One token, 4096 x
+// 2048: 5.5 us, most of it the start of a kernel and the way to memory and back.
 #include <cuda.h>  // CUtensorMap
 
 #include <cstring>

@@ -25,8 +25,17 @@
 // recomputed logits).  Where there are too few output tiles to fill the SMs the
 // reduction is split, the partial sums being added in a fixed order.
 //
+// Measured at 2048 tokens, 32000 classes, width 2048 (268 GFLOP a product), each alone:
+// stats 148 us, dlogits 171, dW 156, dh 157 (1.57 to 1.82 PFLOP/s, the tensor pipe 81 to
+// 95 % active); back to back the power limit makes it 870 us in all.  16384 tokens,
+// 50257 classes: 10.9 ms, 1.24 PFLOP/s.  4096 tokens, 32768 classes, width 1024, forward
+// alone: 222 us, where a tile's exponentials outlast half its products.
+//
+// The tensor cores truncate addends as they align them to an fp32 accumulator: loss and
+// lse are good to about 2.5e-6 of their value at widths of 2700 and more.
+//
 // Kernel: persistent, one CTA per SM, warp-specialised: warp 0 streams operand
-// tiles by TMA (128-byte swizzle) through a ring of stages, one thread of warp 1
+// tiles by TMA (128-byte swizzle) through a ring of stages, one lane of warp 1
 // issues tcgen05.mma into two TMEM accumulators in turn, warps 2-9 run the
 // epilogue of the other one.  Every wait is bounded (M3_ERR_TIMEOUT).
 #include <cuda.h>  // CUtensorMap
