@@ -1116,6 +1116,7 @@ cudaError_t group_norm_fwd_launch(const NormArgs& a0, cudaStream_t s) {
   UnitPlan u;
   if (unit_plan(a, false, &u)) return unit_launch(a, u, false, s);
   const SlicePlan p = slice_plan(a, false);
+  if (a.batch * p.tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)(a.batch * p.tiles), (unsigned)p.splits);
   if (p.whole)
     return with_shape(a, p.V, [&](auto bf16, auto v, auto act) {
@@ -1146,6 +1147,7 @@ cudaError_t group_norm_bwd_launch(const NormArgs& a0, cudaStream_t s) {
     return e != cudaSuccess ? e : param_reduce(a, u.yb, s);
   }
   const SlicePlan p = slice_plan(a, true);
+  if (a.batch * p.tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)(a.batch * p.tiles), (unsigned)p.splits);
   const int64_t slices = a.batch * a.groups;
   float2* means = reinterpret_cast<float2*>(a.ws);

@@ -1199,12 +1199,18 @@ w4_quantize_kernel(int64_t N, int64_t K, int G, const void* W, uint8_t* codes,
 
 }  // namespace
 
-cudaError_t w4_launch(const W4Args& a, cudaStream_t s) {
-  switch (a.group) {
-    case 32: return launch_g<32>(a, s);
-    case 64: return launch_g<64>(a, s);
-    default: return launch_g<128>(a, s);
+cudaError_t w4_launch(const W4Args& all, cudaStream_t s) {
+  // tiles of tokens are a grid's second dimension, which ends at 65535
+  constexpr int64_t most = (int64_t)1 << 20;
+  cudaError_t e = cudaSuccess;
+  for (int64_t m = 0; m < all.M && e == cudaSuccess; m += most) {
+    W4Args a = all;
+    a.M = all.M - m < most ? all.M - m : most;
+    a.A = static_cast<const char*>(all.A) + m * all.K * 2;
+    a.out = static_cast<char*>(all.out) + m * all.N * (all.out_f32 ? 4 : 2);
+    e = a.group == 32 ? launch_g<32>(a, s) : a.group == 64 ? launch_g<64>(a, s) : launch_g<128>(a, s);
   }
+  return e;
 }
 
 cudaError_t w4_quantize_launch(int64_t N, int64_t K, int group, bool bf16, const void* W,

@@ -94,7 +94,7 @@ struct GemmArgs {
   const float* dloss;
   __nv_bfloat16* d;       // [M][ldd]
   int64_t ldd;
-  float* unit;            // c: written by dlogits, a factor of out in grads
+  float* unit;            // c: written by the first piece's dlogits, a factor of out in grads
   // grads
   float* acc;             // [splits][M][N] partial sums or running sum
   __nv_bfloat16* out;     // [M][N], written when set
@@ -257,6 +257,7 @@ __device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* ma
 __device__ __forceinline__ float largest_dloss(const GemmArgs& g, float* s_max) {
   const int i = threadIdx.x - 64;
   float c = 0.f;
+#pragma unroll 4
   for (int64_t m = i; m < g.M; m += 32 * kEpiWarps) {
     const int64_t t = g.targets[m];
     if (t != g.ignore && t >= 0 && t < g.V) c = fmaxf(c, fabsf(g.dloss[m]));
@@ -502,8 +503,12 @@ xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
     float unit = 1.f;
     if constexpr (MODE == kDlogits) {
       __shared__ float s_max[kEpiWarps];
-      unit = largest_dloss(g, s_max);
-      if (blockIdx.x == 0 && tid == 64) *g.unit = unit;
+      if (g.dependent) {  // a later piece
+        unit = *g.unit;
+      } else {
+        unit = largest_dloss(g, s_max);
+        if (blockIdx.x == 0 && tid == 64) *g.unit = unit;
+      }
     }
     if constexpr (MODE == kGrad) unit = *g.unit;
     int j = 0;

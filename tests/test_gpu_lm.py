@@ -793,3 +793,17 @@ def test_autograd_loss_reductions_and_frozen_head():
     empty.backward()
     assert float(empty) == 0.0
     ok()
+
+
+def test_w4_more_tokens_than_a_grid_counts():
+    """2^20 + 5 and 5 000 000 tokens (the tiles of a grid's second dimension are 65535 at
+    most): the last tokens' outputs, and the ones on both sides of a cut."""
+    W = (torch.randn((3, 32), generator=torch.Generator().manual_seed(1))).cuda()
+    codes, scales, zeros = m3.m3_w4_quantize(W, 32)
+    for M in ((1 << 20) + 5, 5_000_000):
+        A = torch.randn((M, 32), device="cuda").bfloat16()
+        out = m3.m3_linear_w4(A, codes, scales, zeros, out_dtype=torch.float32)
+        ok()
+        for a, b in ((0, 40), ((1 << 20) - 20, min((1 << 20) + 20, M)), (M - 40, M)):
+            want = m3.m3_linear_w4(A[a:b].clone(), codes, scales, zeros, out_dtype=torch.float32)
+            assert torch.equal(out[a:b], want)
