@@ -445,7 +445,7 @@ M3_API int m3_group_norm_bwd_varlen(const m3_norm_shape* shape, const int32_t* c
  *   lse_t = log sum_v exp(h_t . W_v),  loss_t = lse_t - h_t . W_{target_t},
  *   0 where target_t == ignore_index;
  *   m3_linear_xent_bwd: gradients of sum_t loss_t dloss_t; an ignored token
- *   contributes none (its dloss is not read).
+ *   contributes none, whatever its dloss and h hold.
  *   tokens >= 0, vocab >= 1, width >= 8 with width % 8 == 0; tokens, vocab,
  *   width < 2^31 - 256.
  *   h        [tokens][width] bf16;  W [vocab][width] bf16 (the [out][in]

@@ -94,6 +94,9 @@ struct GemmArgs {
   const float* dloss;
   __nv_bfloat16* d;       // [M][ldd]
   int64_t ldd;
+  const __nv_bfloat16* h; // [M][K], copied by the first piece's dlogits
+  __nv_bfloat16* scored;  // to here with zeros for the tokens that are not scored, or nullptr
+  int64_t K;
   float* unit;            // c: written by the first piece's dlogits, a factor of out in grads
   // grads
   float* acc;             // [splits][M][N] partial sums or running sum
@@ -270,6 +273,25 @@ __device__ __forceinline__ float largest_dloss(const GemmArgs& g, float* s_max) 
 #pragma unroll
   for (int w = 1; w < kEpiWarps; ++w) c = fmaxf(c, s_max[w]);
   return c > 0.f && c < INFINITY ? c : 1.f;
+}
+
+// The hidden states that dW = d^T h is taken from: d is 0 in a token that is not
+// scored, but 0 times a NaN or an infinity that stands there (padding) is not.
+// Done by the warps that wait for the first tile: 2 M K bytes read and written.
+__device__ __forceinline__ void copy_scored(const GemmArgs& g) {
+  const int warp = (threadIdx.x - 64) >> 5, lane = threadIdx.x & 31;
+  const int nvec = (int)(g.K / 8);
+  for (int64_t m = (int64_t)blockIdx.x * kEpiWarps + warp; m < g.M; m += (int64_t)gridDim.x * kEpiWarps) {
+    const int64_t t = g.targets[m];
+    const bool live = t != g.ignore && t >= 0 && t < g.V;
+    const uint4* from = reinterpret_cast<const uint4*>(g.h + m * g.K);
+    uint4* to = reinterpret_cast<uint4*>(g.scored + m * g.K);
+#pragma unroll 4
+    for (int v = lane; v < nvec; v += 32) {
+      const uint4 x = from[v];  // does not wait for the target
+      to[v] = live ? x : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
 }
 
 template <int MODE, int BN>
@@ -508,6 +530,7 @@ xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
       } else {
         unit = largest_dloss(g, s_max);
         if (blockIdx.x == 0 && tid == 64) *g.unit = unit;
+        if (g.scored) copy_scored(g);
       }
     }
     if constexpr (MODE == kGrad) unit = *g.unit;
@@ -688,9 +711,12 @@ cudaError_t gemm_cg(const GemmArgs& g0, const Operand& a, const Operand& b, cuda
   e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t)g.mt * g.nt * g.splits;
-  return launch_kernel(kern, dim3((unsigned)(CG * (tiles < sms / CG ? tiles : sms / CG))), kThreads,
-                       C::SMEM, s, g.dependent, CG, g, maps);
+  int64_t ctas = (int64_t)g.mt * g.nt * g.splits;
+  // tokens are copied a warp each: CTAs without a tile help
+  if (MODE == kDlogits && g.scored && !g.dependent && ctas < ceil_div(g.M, CG * kEpiWarps))
+    ctas = ceil_div(g.M, CG * kEpiWarps);
+  if (ctas > sms / CG) ctas = sms / CG;
+  return launch_kernel(kern, dim3((unsigned)(CG * ctas)), kThreads, C::SMEM, s, g.dependent, CG, g, maps);
 }
 
 template <int MODE, bool AMN, bool BMN>
@@ -755,7 +781,7 @@ struct BwdPlan {
   int64_t piece, ldd;  // classes of one piece, and its row length (a multiple of 64)
   int pieces;
   Cut dh, dw;
-  size_t d_bytes, dh_bytes, dw_bytes;
+  size_t d_bytes, dh_bytes, dw_bytes, h_bytes;
 };
 
 BwdPlan bwd_plan(const XentArgs& a) {
@@ -773,6 +799,7 @@ BwdPlan bwd_plan(const XentArgs& a) {
   p.dh_bytes = p.pieces > 1 || p.dh.splits > 1
                    ? align_up((size_t)p.dh.splits * a.M * a.K * 4, 256) : 0;
   p.dw_bytes = p.dw.splits > 1 ? align_up((size_t)p.dw.splits * p.piece * a.K * 4, 256) : 0;
+  p.h_bytes = align_up((size_t)a.M * a.K * 2, 256);
   return p;
 }
 
@@ -796,7 +823,7 @@ size_t xent_workspace(const XentArgs& a, bool backward) {
   if (a.M == 0) return 0;
   if (!backward) return fwd_stat_bytes(a) + align_up((size_t)a.M * 4, 256);
   const BwdPlan p = bwd_plan(a);
-  return p.d_bytes + p.dh_bytes + p.dw_bytes + 256;
+  return p.d_bytes + p.dh_bytes + p.dw_bytes + p.h_bytes + 256;
 }
 
 cudaError_t xent_fwd_launch(const XentArgs& a, cudaStream_t s) {
@@ -822,7 +849,8 @@ cudaError_t xent_bwd_launch(const XentArgs& a, cudaStream_t s) {
   __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(a.ws);
   float* dh32 = reinterpret_cast<float*>(a.ws + p.d_bytes);
   float* dw32 = reinterpret_cast<float*>(a.ws + p.d_bytes + p.dh_bytes);
-  float* unit = reinterpret_cast<float*>(a.ws + p.d_bytes + p.dh_bytes + p.dw_bytes);
+  __nv_bfloat16* scored = reinterpret_cast<__nv_bfloat16*>(a.ws + p.d_bytes + p.dh_bytes + p.dw_bytes);
+  float* unit = reinterpret_cast<float*>(a.ws + p.d_bytes + p.dh_bytes + p.dw_bytes + p.h_bytes);
   for (int i = 0; i < p.pieces; ++i) {
     const int64_t v0 = (int64_t)i * p.piece, n = a.V - v0 < p.piece ? a.V - v0 : p.piece;
     const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.W) + v0 * a.K;
@@ -840,6 +868,9 @@ cudaError_t xent_bwd_launch(const XentArgs& a, cudaStream_t s) {
     g.d = d;
     g.ldd = p.ldd;
     g.unit = unit;
+    g.h = static_cast<const __nv_bfloat16*>(a.h);
+    g.scored = a.dW ? scored : nullptr;
+    g.K = a.K;
     cudaError_t e = gemm<kDlogits, false, false>(g, Operand{a.h, a.M, a.K, a.K},
                                                  Operand{W, n, a.K, a.K}, s);
     if (e != cudaSuccess) return e;
@@ -852,7 +883,7 @@ cudaError_t xent_bwd_launch(const XentArgs& a, cudaStream_t s) {
       w.unit = unit;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dW) + v0 * a.K;
       if (w.splits > 1) w.acc = dw32; else w.out = out;
-      e = gemm<kGrad, true, true>(w, Operand{d, a.M, n, p.ldd}, Operand{a.h, a.M, a.K, a.K}, s);
+      e = gemm<kGrad, true, true>(w, Operand{d, a.M, n, p.ldd}, Operand{scored, a.M, a.K, a.K}, s);
       if (e == cudaSuccess && w.splits > 1) e = sum_splits(dw32, w.splits, n * a.K, unit, out, s);
       if (e != cudaSuccess) return e;
     }

@@ -365,6 +365,24 @@ def test_xent_large_logits_and_one_gradient_only():
     assert only_w[0] is None and torch.equal(only_w[1], dW)
 
 
+@pytest.mark.parametrize("M,V,K", [(70, 300, 64), (600, 9000, 136)])
+def test_xent_tokens_not_scored_may_hold_anything(M, V, K):
+    """NaN and infinities in the hidden states and dloss of ignored tokens (padding):
+    their loss and dh are 0, and dW is the one without them."""
+    h, W, t, dl = xent_inputs(M, V, K, 11, ignored=0.4)
+    off = (t < 0).nonzero()[:, 0]
+    clean = [v.clone() for v in (h, dl)]
+    h[off[0::3]], h[off[1::3]], dl[off[::2]] = float("nan"), float("inf"), float("nan")
+    clean[0][off], clean[1][off] = 0, 0
+    d = [v.cuda() for v in (h, W, t, dl)]
+    loss, lse = m3.m3_linear_xent_fwd(*d[:3])
+    dh, dW = m3.m3_linear_xent_bwd(*d[:3], lse, d[3])
+    ok()
+    assert (loss[off.cuda()] == 0).all() and (dh[off.cuda()] == 0).all()
+    lse[off.cuda()] = torch.from_numpy(lm.xent(clean[0], W, t)["lse"])[off].float().cuda()
+    check_xent(clean[0], W, t, clean[1], loss, lse, dh, dW)
+
+
 def test_xent_no_token():
     h, W = torch.zeros((0, 64), dtype=torch.bfloat16).cuda(), torch.randn((10, 64)).bfloat16().cuda()
     t = torch.zeros(0, dtype=torch.long).cuda()
