@@ -275,6 +275,24 @@ __device__ __forceinline__ float largest_dloss(const GemmArgs& g, float* s_max) 
   return c > 0.f && c < INFINITY ? c : 1.f;
 }
 
+// Lane j of four gets the others' w[j]: w[i] becomes lane i's w[j].
+__device__ __forceinline__ void turn4(uint4 (&w)[4], int lane) {
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & o) continue;
+      uint4 &a = w[i], &b = w[i | o];
+      const uint4 give = up ? a : b;
+      const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, o), __shfl_xor_sync(0xffffffffu, give.y, o),
+                                   __shfl_xor_sync(0xffffffffu, give.z, o), __shfl_xor_sync(0xffffffffu, give.w, o));
+      if (up) a = got;
+      else b = got;
+    }
+  }
+}
+
 // The hidden states that dW = d^T h is taken from: d is 0 in a token that is not
 // scored, but 0 times a NaN or an infinity that stands there (padding) is not.
 // Done by the warps that wait for the first tile: 2 M K bytes read and written.
@@ -353,7 +371,6 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const Tile& t, int64
       uint32_t v[32];
       tmem_ld32(tcol + (uint32_t)c, v);
       tmem_ld_wait();
-      if (!on) continue;
       float f[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
@@ -361,13 +378,20 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const Tile& t, int64
         if (rel == c + e) p -= 1.f;
         f[e] = live ? p * scale : 0.f;
       }
-      __nv_bfloat16* o = g.d + m * g.ldd + n0 + c;
+      uint4 w[4];
 #pragma unroll
-      for (int e = 0; e < 32; e += 8)
-        if (n0 + c + e < g.ldd && M3_IN(m * g.ldd + n0 + c + e + 7, g.M * g.ldd, g.status))
-          *reinterpret_cast<uint4*>(o + e) =
-              make_uint4(pack_bf16(f[e], f[e + 1]), pack_bf16(f[e + 2], f[e + 3]),
-                         pack_bf16(f[e + 4], f[e + 5]), pack_bf16(f[e + 6], f[e + 7]));
+      for (int i = 0; i < 4; ++i)
+        w[i] = make_uint4(pack_bf16(f[8 * i], f[8 * i + 1]), pack_bf16(f[8 * i + 2], f[8 * i + 3]),
+                          pack_bf16(f[8 * i + 4], f[8 * i + 5]), pack_bf16(f[8 * i + 6], f[8 * i + 7]));
+      // four lanes turn their rows' pieces about, so that a store writes 64 bytes of a row
+      turn4(w, lane);
+      const int64_t n = n0 + c + 8 * (lane & 3);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t row = m - (lane & 3) + i;
+        if (row < g.M && n < g.ldd && M3_IN(row * g.ldd + n + 7, g.M * g.ldd, g.status))
+          *reinterpret_cast<uint4*>(g.d + row * g.ldd + n) = w[i];
+      }
     }
   } else {
     float* acc = g.acc ? g.acc + ((int64_t)t.split * g.M + m) * g.N + n0 : nullptr;
