@@ -394,35 +394,54 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const Tile& t, int64
       }
     }
   } else {
-    float* acc = g.acc ? g.acc + ((int64_t)t.split * g.M + m) * g.N + n0 : nullptr;
-    __nv_bfloat16* out = g.out ? g.out + m * g.N + n0 : nullptr;
+    // as above: after the exchange a lane holds its piece of four rows
+    const int64_t first = m - (lane & 3);
 #pragma unroll 1
     for (int c = 0; c < BN / 2; c += 32) {
       uint32_t v[32];
       tmem_ld32(tcol + (uint32_t)c, v);
       tmem_ld_wait();
-      if (!on) continue;
+      if (!g.acc) {
+        uint4 w[4];
 #pragma unroll
-      for (int e = 0; e < 32; e += 8) {  // N is a multiple of 8
-        if (n0 + c + e >= g.N || !M3_IN(m * g.N + n0 + c + e + 7, g.M * g.N, g.status)) continue;
-        float f[8];
+        for (int i = 0; i < 4; ++i) {
+          float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[e + i]);
-        if (g.add) {
-          const float4 x = *reinterpret_cast<const float4*>(acc + c + e);
-          const float4 y = *reinterpret_cast<const float4*>(acc + c + e + 4);
-          f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
-          f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+          for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * i + e]) * unit;
+          w[i] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                            pack_bf16(f[6], f[7]));
         }
-        if (out) {
+        turn4(w, lane);
+        const int64_t n = n0 + c + 8 * (lane & 3);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] *= unit;
-          *reinterpret_cast<uint4*>(out + c + e) =
-              make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                         pack_bf16(f[6], f[7]));
-        } else {
-          *reinterpret_cast<float4*>(acc + c + e) = make_float4(f[0], f[1], f[2], f[3]);
-          *reinterpret_cast<float4*>(acc + c + e + 4) = make_float4(f[4], f[5], f[6], f[7]);
+        for (int i = 0; i < 4; ++i)  // N is a multiple of 8
+          if (first + i < g.M && n < g.N && M3_IN((first + i) * g.N + n + 7, g.M * g.N, g.status))
+            *reinterpret_cast<uint4*>(g.out + (first + i) * g.N + n) = w[i];
+        continue;
+      }
+#pragma unroll
+      for (int h = 0; h < 32; h += 16) {
+        uint4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = make_uint4(v[h + 4 * i], v[h + 4 * i + 1], v[h + 4 * i + 2], v[h + 4 * i + 3]);
+        turn4(w, lane);
+        const int64_t n = n0 + c + h + 4 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (first + i >= g.M || n >= g.N || !M3_IN((first + i) * g.N + n + 3, g.M * g.N, g.status)) continue;
+          float4* acc = reinterpret_cast<float4*>(g.acc + ((int64_t)t.split * g.M + first + i) * g.N + n);
+          float4 f = make_float4(__uint_as_float(w[i].x), __uint_as_float(w[i].y), __uint_as_float(w[i].z),
+                                 __uint_as_float(w[i].w));
+          if (g.add) {
+            const float4 x = *acc;
+            f.x += x.x; f.y += x.y; f.z += x.z; f.w += x.w;
+          }
+          if (g.out)
+            *reinterpret_cast<uint2*>(g.out + (first + i) * g.N + n) =
+                make_uint2(pack_bf16(f.x * unit, f.y * unit), pack_bf16(f.z * unit, f.w * unit));
+          else
+            *acc = f;
         }
       }
     }
