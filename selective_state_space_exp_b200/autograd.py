@@ -19,6 +19,8 @@ to nearest even once, at the end; dt, A, lam, theta, h0 are fp32).
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import m3
@@ -32,6 +34,37 @@ def _dy(dy, x):
     if dy.dtype != x.dtype and dy.dtype != torch.float32:
         dy = dy.float()
     return dy.contiguous()
+
+
+class _NoDerivative(torch.autograd.Function):
+    """Identity on a gradient that the library computed; its own derivative raises."""
+
+    @staticmethod
+    def forward(ctx, what, g, *roots):
+        ctx.what = what
+        return g
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError(f"{ctx.what} has first derivatives only: a gradient it gave (create_graph=True) "
+                           "cannot be differentiated again")
+
+
+def _first_derivative(backward):
+    """Marks a backward that is no differentiable function itself.  With create_graph its
+    gradients hang on the inputs by a node that raises, so a term made from them is never
+    left out in silence.  (torch's once_differentiable lets them go without history where
+    the incoming gradient has none, as below a plain sum.)"""
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        if not torch.is_grad_enabled():
+            return backward(ctx, *grads)
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        roots = [t for t in (*ctx.saved_tensors, *grads) if t is not None and t.requires_grad]
+        return tuple(None if g is None else _NoDerivative.apply(type(ctx).__name__, g, *roots) for g in out)
+
+    return run
 
 
 class M3Scan(torch.autograd.Function):
@@ -124,6 +157,7 @@ class M3GroupNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_first_derivative
     def backward(ctx, dy):
         cu, x, weight, bias, z, mean, rstd = ctx.saved_tensors
         dy = dy.to(x.dtype).contiguous()
@@ -152,14 +186,15 @@ def _outside(cu_seqlens, total):
 def group_norm(x, groups: int, weight=None, bias=None, z=None, *, act="none", eps: float = 1e-5,
                scope="token"):
     """Differentiable m3.m3_group_norm_fwd: y alone, gradients of x, weight, bias
-    and z by m3_group_norm_bwd (weight and bias fp32)."""
+    and z by m3_group_norm_bwd (weight and bias fp32).  First derivatives only: a
+    second one raises."""
     return M3GroupNorm.apply(None, None, groups, act, eps, scope, x, weight, bias, z)
 
 
 def group_norm_varlen(cu_seqlens, x, groups: int, weight=None, bias=None, z=None, *, act="none",
                       eps: float = 1e-5, max_seqlen=None):
     """group_norm over the sequences of a packed batch (x [T][C]); rows outside
-    every sequence pass through unchanged."""
+    every sequence pass through unchanged.  First derivatives only."""
     if max_seqlen is None:
         max_seqlen = int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item())
     return M3GroupNorm.apply(cu_seqlens, max_seqlen, groups, act, eps, "sequence", x, weight,
@@ -175,6 +210,7 @@ class M3LinearXent(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @_first_derivative
     def backward(ctx, dloss):
         targets, h, W, lse = ctx.saved_tensors
         dh, dW = m3.m3_linear_xent_bwd(h, W, targets, lse, dloss.contiguous(),
@@ -188,7 +224,8 @@ def linear_cross_entropy(h, W, targets, *, ignore_index: int = -100, reduction="
     """Softmax cross entropy of the head W [V][K] on hidden states h [..][K]
     (bf16) without the logits, by m3_linear_xent_fwd / _bwd.  reduction "none"
     (shaped like targets), "sum", or "mean" over the scored tokens (0 where there
-    is none).  Gradients of h and W, in bf16."""
+    is none).  Gradients of h and W, in bf16; first derivatives only: a second one
+    raises."""
     if reduction not in ("none", "sum", "mean"):
         raise ValueError(f"reduction is {reduction!r}: expected 'none', 'sum' or 'mean'")
     loss = M3LinearXent.apply(ignore_index, targets, h, W)
