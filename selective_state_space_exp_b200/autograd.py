@@ -16,6 +16,7 @@ C ABI's M3_FLAG_DY_F32).  The final-state gradient is fp32.  The backward
 computes every gradient in fp32; each is returned in its input's dtype, as
 torch requires (bf16 x, B, C, B_prev, x_prev receive bf16 gradients, rounded
 to nearest even once, at the end; dt, A, lam, theta, h0 are fp32).
+First derivatives only, here and below: a second one raises.
 """
 from __future__ import annotations
 
@@ -76,6 +77,7 @@ class M3Scan(torch.autograd.Function):
         return y, fs
 
     @staticmethod
+    @_first_derivative
     def backward(ctx, dy, d_final):
         x, dt, A, lam, theta, B, C, h0, B_prev, x_prev = ctx.saved_tensors
         if dy is None:
@@ -110,6 +112,7 @@ class M3ScanVarlen(torch.autograd.Function):
         return y, fs
 
     @staticmethod
+    @_first_derivative
     def backward(ctx, dy, d_final):
         cu, x, dt, A, lam, theta, B, C, h0, B_prev, x_prev = ctx.saved_tensors
         if dy is None:

@@ -103,3 +103,23 @@ def test_second_derivatives_of_the_loss_raise(calls):
         for g in torch.autograd.grad(loss.sum(), (h, W), create_graph=True):
             with pytest.raises(RuntimeError, match="first derivatives only"):
                 g.square().sum().backward(retain_graph=True)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_second_derivatives_of_the_scan_raise(monkeypatch, packed):
+    """Stand-ins with the right shapes are enough: the gradients' history is looked at."""
+    names = ("x", "dt", "A", "lam", "theta", "B", "C", "h0", "B_prev", "x_prev")
+    fwd = lambda *a, **k: (torch.ones(3), torch.ones(2))  # noqa: E731
+    bwd = lambda *a, **k: {n: torch.ones(3) for n in names}  # noqa: E731
+    for name in ("m3_scan_fwd", "m3_scan_fwd_varlen"):
+        monkeypatch.setattr(m3, name, fwd)
+    for name in ("m3_scan_bwd", "m3_scan_bwd_varlen"):
+        monkeypatch.setattr(m3, name, bwd)
+    args = [torch.ones(3).requires_grad_() for _ in range(7)]
+    if packed:
+        y, state = autograd.m3_scan_varlen(torch.tensor([0, 3], dtype=torch.int32), *args)
+    else:
+        y, state = autograd.m3_scan(*args)
+    for g in torch.autograd.grad(y.sum() + state.sum(), args, create_graph=True):
+        with pytest.raises(RuntimeError, match="first derivatives only"):
+            g.square().sum().backward(retain_graph=True)
