@@ -29,12 +29,19 @@ from . import m3
 _NAMES = ("x", "dt", "A", "lam", "theta", "B", "C", "h0", "B_prev", "x_prev")
 
 
+def _aligned(t):
+    """t as the library takes it, contiguous and on a 16-byte boundary.  The engine may hand
+    over a part of a larger gradient (torch.cat's), which starts anywhere."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _dy(dy, x):
     """dy as the backward reads it: x's dtype, or fp32 unrounded (anything else
     is converted to fp32 first, which is exact for every narrower float)."""
     if dy.dtype != x.dtype and dy.dtype != torch.float32:
         dy = dy.float()
-    return dy.contiguous()
+    return _aligned(dy)
 
 
 class _NoDerivative(torch.autograd.Function):
@@ -84,7 +91,7 @@ class M3Scan(torch.autograd.Function):
             dy = torch.zeros_like(x)
         g = m3.m3_scan_bwd(x, dt, A, lam, theta, B, C, _dy(dy, x), ctx.chunk,
                            h0, B_prev, x_prev,
-                           None if d_final is None else d_final.contiguous().float())
+                           None if d_final is None else _aligned(d_final.float()))
         inputs = dict(zip(_NAMES, (x, dt, A, lam, theta, B, C, h0, B_prev, x_prev)))
         out = [None]  # chunk
         for i, name in enumerate(_NAMES):
@@ -119,7 +126,7 @@ class M3ScanVarlen(torch.autograd.Function):
             dy = torch.zeros_like(x)
         g = m3.m3_scan_bwd_varlen(cu, x, dt, A, lam, theta, B, C, _dy(dy, x),
                                   ctx.chunk, h0, B_prev, x_prev,
-                                  None if d_final is None else d_final.contiguous().float(),
+                                  None if d_final is None else _aligned(d_final.float()),
                                   max_seqlen=ctx.max_seqlen)
         inputs = dict(zip(_NAMES, (x, dt, A, lam, theta, B, C, h0, B_prev, x_prev)))
         out = [None, None, None]  # chunk, max_seqlen, cu_seqlens
@@ -163,7 +170,7 @@ class M3GroupNorm(torch.autograd.Function):
     @_first_derivative
     def backward(ctx, dy):
         cu, x, weight, bias, z, mean, rstd = ctx.saved_tensors
-        dy = dy.to(x.dtype).contiguous()
+        dy = _aligned(dy.to(x.dtype))
         kw = dict(weight=weight, bias=bias, z=z, act=ctx.act)
         if cu is None:
             g = m3.m3_group_norm_bwd(x, ctx.groups, mean, rstd, dy, scope=ctx.scope, **kw)

@@ -123,3 +123,20 @@ def test_second_derivatives_of_the_scan_raise(monkeypatch, packed):
     for g in torch.autograd.grad(y.sum() + state.sum(), args, create_graph=True):
         with pytest.raises(RuntimeError, match="first derivatives only"):
             g.square().sum().backward(retain_graph=True)
+
+
+def test_gradients_off_a_16_byte_boundary_are_copied(calls, monkeypatch):
+    """The gradient of one part of a torch.cat is a contiguous view that may start anywhere."""
+    for f in norm_calls(T=3, C=10).values():
+        x, w, b, z = (t.requires_grad_() for t in (randn(3, 10), randn(10), randn(10, seed=1), randn(3, 10, seed=2)))
+        torch.cat([torch.zeros((1, 10)), f(x, w, b, z)]).square().sum().backward()
+        dy = calls.pop()["dy"]
+        assert dy.is_contiguous() and dy.data_ptr() % 16 == 0
+    grads = []
+    monkeypatch.setattr(m3, "m3_scan_fwd", lambda *a, **k: (torch.ones((3, 2)), torch.ones((3, 2))))
+    monkeypatch.setattr(m3, "m3_scan_bwd", lambda *a: grads.append((a[7], a[12])) or {"x": torch.ones((3, 2))})
+    x = torch.ones((3, 2)).requires_grad_()
+    y, state = autograd.m3_scan(x, *[torch.ones((3, 2))] * 6)
+    torch.cat([torch.zeros((1, 2)), y, state]).square().sum().backward()
+    for g in grads[0]:
+        assert g.is_contiguous() and g.data_ptr() % 16 == 0
