@@ -882,7 +882,7 @@ def m3_linear_w4(A, codes, scales, zeros=None, bias=None, *, out=None, out_dtype
     shape = A.shape
     if not shape or shape[-1] != K:
         raise ValueError(f"A is {tuple(shape)}: expected [..][{K}]")
-    if ng == 0 or K % ng != 0:
+    if ng == 0 or K == 0 or K % ng != 0:
         raise ValueError(f"scales is {tuple(scales.shape)} for {K} inputs")
     dev = _device_of(A)
     if out is not None:

@@ -220,3 +220,9 @@ def test_binding_refuses_before_the_library():
                         torch.zeros((4, 3), dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="reduction"):
         autograd.linear_cross_entropy(h, W, t, reduction="max")
+
+
+def test_w4_without_inputs_is_refused():
+    with pytest.raises(ValueError, match="0 inputs"):
+        m3.m3_linear_w4(torch.zeros((1, 0), dtype=torch.bfloat16), torch.zeros((4, 0), dtype=torch.uint8),
+                        torch.zeros((4, 1), dtype=torch.bfloat16))
