@@ -32,9 +32,10 @@
 // 8 sequences x 2048 x 2048, 32 groups, SiLU 46 us forward and 86 us backward (each
 // of their four passes at 4.5 to 5 TB/s, two joining launches at about 5 us).
 // Statistics are fp32: in the unit kernels the mean first, then the deviations
-// from it (whose own mean corrects it) and their squares; in the others sums about
-// one of the values, merged pairwise as counts, means and squared deviations (Chan,
-// Golub and LeVeque): a large common offset is not squared.  No atomics: dw and db are
+// from it (whose own mean corrects it) and their squares; in the others sums about a
+// reference that follows each thread's mean, joined as counts, means and squared
+// deviations (Chan, Golub and LeVeque): neither a large common offset nor an outlier among
+// the first values costs the others their squares.  No atomics: dw and db are
 // partial sums in the workspace, added in a fixed order.  y, dx and dz are rounded to
 // the io type once, at their store.
 #include <type_traits>
@@ -557,20 +558,27 @@ __device__ __forceinline__ int64_t group_of(const NormArgs& a, const SlicePlan& 
   return p.pieces > 1 ? o.tile / p.pieces : (int64_t)o.tile * p.gpt + i;
 }
 
-// The rows of a thread, AHEAD at a time: load(u, at) of all of them, then use(u,
-// at) of each.  at: element of the thread's vector.
-template <int AHEAD, typename Load, typename Use>
+// Rows of a thread.
+__device__ __forceinline__ int rows_of_thread(const SlicePlan& p, const Place& o) {
+  return o.r0 + o.ty < o.r1 ? ((int)(o.r1 - o.r0) - o.ty + p.ty - 1) / p.ty : 0;
+}
+
+// The rows of a thread, AHEAD at a time: load(u, at) of all of them, use(u, at) of
+// each, then pause(rows so far).  at: element of the thread's vector.
+template <int AHEAD, typename Load, typename Use, typename Pause>
 __device__ __forceinline__ void over_rows(const NormArgs& a, const SlicePlan& p, const Place& o,
-                                          Load&& load, Use&& use) {
+                                          Load&& load, Use&& use, Pause&& pause) {
   const int64_t next = p.ty * a.channels;
   int64_t at = (o.base + o.r0 + o.ty) * a.channels + o.col;
-  int left = o.r0 + o.ty < o.r1 ? ((int)(o.r1 - o.r0) - o.ty + p.ty - 1) / p.ty : 0;
+  const int rows = rows_of_thread(p, o);
+  int left = rows;
   for (; left >= AHEAD; left -= AHEAD) {
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) load(u, at + u * next);
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) use(u, at + u * next);
     at += AHEAD * next;
+    pause(rows - left + AHEAD);
   }
 #pragma unroll
   for (int u = 0; u < AHEAD - 1; ++u)
@@ -578,6 +586,11 @@ __device__ __forceinline__ void over_rows(const NormArgs& a, const SlicePlan& p,
 #pragma unroll
   for (int u = 0; u < AHEAD - 1; ++u)
     if (u < left) use(u, at + u * next);
+}
+template <int AHEAD, typename Load, typename Use>
+__device__ __forceinline__ void over_rows(const NormArgs& a, const SlicePlan& p, const Place& o,
+                                          Load&& load, Use&& use) {
+  over_rows<AHEAD>(a, p, o, load, use, [](int) {});
 }
 
 // Sums over the threads of each group of the tile, a warp a group: f(group, sum).
@@ -599,43 +612,104 @@ __device__ __forceinline__ void tile_sums(const SlicePlan& p, float2 c, float2* 
   }
 }
 
+// The moments of the threads of each group of the tile joined, a warp a group: f(group,
+// moments).  The means' mean first, then what is left about it: all of it positive.
+template <typename F>
+__device__ __forceinline__ void tile_moments(const SlicePlan& p, const Moments& m, Moments* s_m, F&& f) {
+  s_m[threadIdx.x] = m;
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wide = p.tx / p.gpt, count = wide * p.ty;
+  for (int i = warp; i < p.gpt; i += kThreads / 32) {
+    const Moments* at = s_m + i * wide;
+    auto of = [&](int k) -> const Moments& {  // neighbours where a group has all threads, or all of a row
+      return p.ty == 1 || p.gpt == 1 ? at[k] : at[(k / wide) * p.tx + k % wide];
+    };
+    const float first = at->mean;  // that thread has rows if any has
+    float n = 0.f, e = 0.f;
+    for (int k = lane; k < count; k += 32) {
+      const Moments& q = of(k);
+      n += q.n;
+      e = fmaf(q.n, q.mean - first, e);
+    }
+    n = lane_sum(n, 32);
+    e = lane_sum(e, 32);
+    if (n == 0.f) {
+      if (lane == 0) f(i, Moments{0.f, 0.f, 0.f});
+      continue;
+    }
+    const float mean = first + __fdividef(e, n);
+    e = 0.f;
+    float m2 = 0.f;
+    for (int k = lane; k < count; k += 32) {
+      const Moments& q = of(k);
+      const float d = q.mean - mean, nd = q.n * d;
+      e += nd;
+      m2 += fmaf(nd, d, q.m2);
+    }
+    e = lane_sum(e, 32);
+    m2 = lane_sum(m2, 32);
+    const float d = __fdividef(e, n);
+    if (lane == 0) f(i, Moments{n, mean + d, fmaf(-d, e, m2)});
+  }
+}
+
 // The moments of each group of the tile over the block's rows: f(group of the tile,
 // group, moments).
+//
+// A thread sums deviations and their squares about a reference that follows its mean:
+// the mean of its first vector, and whenever it has seen as many rows again the mean so
+// far.  What a sum then loses is a part of the values' own squares, wherever an outlier
+// stands among them: with n values about the old reference and n more, whose means differ
+// by 2 d, the squares hold at least 4 n d^2 and the move takes 2 n d^2 off.  Sums about the
+// group's first value (one pivot for the block) lost 1e-4 to 1e-3 of rstd where that value
+// was 300 deviations out, in an emulation of their order.  Forward in bf16 against them:
+// 8 x 2048 x 2048 44.3 us, as before; 16 x 256 x 2048 11.9 against 11.3.
 template <bool BF16, int V, int AHEAD, typename F>
 __device__ __forceinline__ void stats_pass(const NormArgs& a, const SlicePlan& p, const Place& o, F&& f) {
   using X = Io<BF16, V>;
-  // sums about the group's first value in this split: it lies among the values,
-  // so the squares cannot be lost under it
-  float2 s1 = both(0.f), s2 = both(0.f);
-  auto pivot_of = [&](int64_t g) {
-    const int64_t at = (o.base + o.r0) * a.channels + g * a.cg;
-    return o.r0 < o.r1 ? io_load(a.x, at, BF16) : 0.f;
-  };
-  if (o.on) {
-    const float pivot = pivot_of(group_of(a, p, o, o.group));
+  const int rows = o.on ? rows_of_thread(p, o) : 0;
+  Moments m{0.f, 0.f, 0.f};
+  if (rows > 0) {
+    float2 s1 = both(0.f), s2 = both(0.f), v[X::P];
+    X::unpack(X::load(a.x, (o.base + o.r0 + o.ty) * a.channels + o.col), v);
+#pragma unroll
+    for (int e = 0; e < X::P; ++e) s1 = fadd2(s1, v[e]);
+    float ref = (s1.x + s1.y) * (1.f / V);
+    s1 = both(0.f);
+    float sq = 0.f;     // s2 of the rows before the last pause: short sums, then their sum
+    int moved = AHEAD;  // rows at which the reference moves next
     typename X::R raw[AHEAD];
     over_rows<AHEAD>(a, p, o, [&](int u, int64_t at) { raw[u] = X::load(a.x, at); },
-                          [&](int u, int64_t) {
-                            float2 v[X::P];
-                            X::unpack(raw[u], v);
+                     [&](int u, int64_t) {
+                       X::unpack(raw[u], v);
 #pragma unroll
-                            for (int e = 0; e < X::P; ++e) {
-                              const float2 d = minus<V>(v[e], pivot);
-                              s1 = fadd2(s1, d);
-                              s2 = ffma2(d, d, s2);
-                            }
-                          });
+                       for (int e = 0; e < X::P; ++e) {
+                         const float2 d = minus<V>(v[e], ref);
+                         s1 = fadd2(s1, d);
+                         s2 = ffma2(d, d, s2);
+                       }
+                     },
+                     [&](int seen) {
+                       sq += s2.x + s2.y;
+                       s2 = both(0.f);
+                       if (seen != moved) return;
+                       moved = 2 * seen;
+                       const float n = (float)seen * V, e = s1.x + s1.y;
+                       const float to = ref + __fdividef(e, n), d = to - ref;
+                       const float left = fmaf(-n, d, e);  // of the sum about the new one
+                       sq = fmaf(-d, e + left, sq);
+                       s1 = make_float2(left, 0.f);
+                       ref = to;
+                     });
+    const float n = (float)rows * V, e = s1.x + s1.y, d = __fdividef(e, n);
+    const float m2 = fmaf(-d, e, sq + (s2.x + s2.y));
+    m = Moments{n, ref + d, m2 < 0.f ? 0.f : m2};
   }
-  __shared__ float2 s_c[kThreads];
-  tile_sums(p, make_float2(s1.x + s1.y, s2.x + s2.y), s_c, [&](int i, float2 c) {
+  __shared__ Moments s_m[kThreads];
+  tile_moments(p, m, s_m, [&](int i, const Moments& t) {
     const int64_t g = group_of(a, p, o, i);
-    if (g >= a.groups) return;
-    // values of the group in this block: its rows times its channels here
-    const int64_t nvec = a.cg / V, first = (int64_t)o.piece * p.tx;
-    const int64_t vecs = p.pieces > 1 ? (nvec - first < p.tx ? nvec - first : p.tx) : nvec;
-    const float n = (float)((o.r1 - o.r0) * vecs * V);
-    const float d = n > 0.f ? c.x / n : 0.f;
-    f(i, g, Moments{n, pivot_of(g) + d, fmaf(-d, c.x, c.y)});
+    if (g < a.groups) f(i, g, t);
   });
 }
 

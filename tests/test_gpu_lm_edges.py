@@ -1,0 +1,89 @@
+"""The grouped norm, the head's cross entropy and the 4-bit products on the GPU, at
+inputs and in uses where they could go wrong and that test_gpu_lm.py does not reach,
+against the same fp64 oracle (oracle/m3_lm.py)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import m3_lm as lm
+from selective_state_space_exp_b200 import m3
+from parity_helpers import need_gpu
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+IO = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def ok():
+    assert m3.m3_stream_status() == 0
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+# ---- statistics with an outlier ----------------------------------------------------
+
+# samples, positions, groups, channels of a group.  One block makes both passes; one block
+# a tile, but too many rows a thread for both; several blocks a sample; a group wider than a
+# block; channels of four bytes
+OUTLIER = [(4, 128, 32, 64), (3, 7, 2, 16), (300, 40, 16, 64), (2, 3000, 2, 24), (1, 9000, 1, 8), (3, 61, 1, 4100),
+           (3, 1001, 6, 85)]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("far", [50.0, 300.0, 1000.0])
+@pytest.mark.parametrize("B,L,G,cg", OUTLIER)
+def test_statistics_with_an_outlier_first(B, L, G, cg, far, io):
+    """The first value of every group, or its whole first position, stands far from the
+    others (language models put their largest activations at the first position).
+
+    Sums of squares are of positive terms: 32 in a piece (8 rows x 4 pairs), at most 10
+    pieces of a thread, 8 threads of a lane, 5 steps of lanes and 10 of splits, 65 additions
+    in a chain, and as much again for what the moves of the reference take off: 130 roundings
+    of the variance, 65 of rstd.  The mean's error is as many of the deviation, and one of
+    the mean itself."""
+    g = gen(B + L + G + cg)
+    x = torch.randn((B, L, G, cg), generator=g)
+    x[0::2, 0, :, 0] = far
+    if B > 1:
+        x[1::2, 0] = far
+    x = x.to(IO[io]).view(B, L, G * cg)
+    y, mean, rstd = m3.m3_group_norm_fwd(x.cuda(), G, scope="sequence")
+    ok()
+    v = f64(x.float()).reshape(B, L, G, cg).transpose(0, 2, 1, 3).reshape(B, G, -1)
+    mu = v.mean(-1)
+    inv = 1 / np.sqrt(((v - mu[..., None]) ** 2).mean(-1) + 1e-5)
+    assert (np.abs(f64(rstd) / inv - 1)).max() <= 72 * U
+    assert (np.abs(f64(mean) - mu) * inv - U * np.abs(mu) * inv).max() <= 72 * U
+    want = (v - mu[..., None]) * inv[..., None]
+    got = f64(y.float()).reshape(B, L, G, cg).transpose(0, 2, 1, 3).reshape(B, G, -1)
+    # xh: 72 roundings from rstd and of the deviation from the mean, a few of its own
+    over = np.abs(got - want) - torch.finfo(IO[io]).eps / 2 * np.abs(want) - 80 * U * (np.abs(want) + 1)
+    assert over.max() <= 0
+
+
+def test_packed_statistics_with_outliers_in_a_long_sequence():
+    """One long sequence among hundreds of short ones: its rows are one block's."""
+    cu = np.concatenate([np.arange(0, 700 * 3, 3), [2100, 2100 + 2000]]).astype(np.int32)
+    T, G, cg = int(cu[-1]), 2, 32
+    x = torch.randn((T, G * cg), generator=gen(3))
+    x[2100] = 1000.0
+    x[::7, 5] = 300.0
+    c = torch.from_numpy(cu).cuda()
+    y, mean, rstd = m3.m3_group_norm_fwd_varlen(c, x.cuda(), G, max_seqlen=2000)
+    ok()
+    ref = lm.group_norm(x, G, spans=list(zip(cu[:-1], cu[1:])))
+    # a thread has 125 rows of the long one: pieces of 8 additions, 31 of them, 8 threads a
+    # lane and 5 steps of lanes, twice for the moves: 104 roundings of the variance
+    assert (np.abs(f64(rstd) / ref["rstd"] - 1)).max() <= 56 * U
+    assert (np.abs(f64(y) - ref["y"]) - 64 * U * (np.abs(ref["y"]) + 1)).max() <= 0
