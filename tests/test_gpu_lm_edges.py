@@ -87,3 +87,64 @@ def test_packed_statistics_with_outliers_in_a_long_sequence():
     # lane and 5 steps of lanes, twice for the moves: 104 roundings of the variance
     assert (np.abs(f64(rstd) / ref["rstd"] - 1)).max() <= 56 * U
     assert (np.abs(f64(y) - ref["y"]) - 64 * U * (np.abs(ref["y"]) + 1)).max() <= 0
+
+
+# ---- parameter gradients over many rows ------------------------------------------------
+
+def parameter_bounds(x, z, dy, w, b, G, act, spans):
+    """fp64 dw and db, and what roundings may move them by, from the sums of the terms'
+    magnitudes.  256 roundings of the sum (a thread, the row slots, the partial rows: far
+    shorter chains), and of each term:
+      xh  8 (|xh| + 1): x - mean and rstd
+      u = xh w + b  |w| of that and 2 (|u| + |b|)
+      g   silu' has a slope of at most 1/2: |dy| (du / 2 + 16 (1 + |u|)), the sigmoid's own
+          error (2^-22 of ex2 and rcp and the exponent's rounding) among the 16; the gate's
+          factor z sigma(z) likewise 16 (1 + |z|)"""
+    ref = lm.group_norm(x, G, w, b, z, act, 1e-5, spans, dy)
+    xs, dys, ws, bs = (lm.f64(v) for v in (x, dy, w, b))
+    C = xs.shape[1]
+    xh = np.zeros_like(xs)
+    for i, (t0, t1) in enumerate(spans):
+        xh[t0:t1] = (xs[t0:t1] - np.repeat(ref["mean"][i], C // G)) * np.repeat(ref["rstd"][i], C // G)
+    u = xh * ws + bs
+    exh = 8 * U * (np.abs(xh) + 1)
+    if act == "silu":
+        s = lm.sigmoid(u)
+        g = dys * s * (1 + u * (1 - s))
+        eg = np.abs(dys) * ((np.abs(ws) * exh + 2 * U * (np.abs(u) + np.abs(bs))) / 2 + 16 * U * (1 + np.abs(u)))
+    elif act == "gate":
+        zs = lm.f64(z)
+        g = dys * zs * lm.sigmoid(zs)
+        eg = np.abs(dys) * 16 * U * (1 + np.abs(zs)) * np.abs(zs)
+    else:
+        g, eg = dys, 0 * dys
+    tw = 256 * U * np.abs(g * xh).sum(0) + (eg * np.abs(xh) + np.abs(g) * exh).sum(0)
+    tb = 256 * U * np.abs(g).sum(0) + eg.sum(0)
+    return ref, tw, tb
+
+
+# samples, positions, groups, channels of a group: one block each, several splits, groups in
+# pieces, and single positions (the unit kernels' partial rows)
+MANY = [(2, 3000, 2, 24), (1, 9000, 1, 8), (1, 8193, 1, 8), (2, 900, 40, 8), (4, 300, 3, 31), (3, 700, 3, 31),
+        (2, 400, 1, 4100), (700, 40, 2, 24), (5000, 1, 6, 8), (3000, 1, 1, 600), (900, 1, 1, 4104)]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ["none", "silu", "gate"])
+@pytest.mark.parametrize("B,L,G,cg", MANY)
+def test_parameter_gradients_over_many_rows(B, L, G, cg, act, io):
+    """Every partial sum counts: the bounds are far below the gradients, which is checked."""
+    g = gen(B * 3 + L + G + cg)
+    C, dt = G * cg, IO[io]
+    x, z, dy = (torch.randn((B * L, C), generator=g).to(dt) for _ in range(3))
+    x = (x * 1.5).to(dt)
+    z = z if act == "gate" else None
+    w, b = torch.randn(C, generator=g) * 0.2 + 1, torch.randn(C, generator=g) * 0.3
+    d = [None if v is None else v.cuda().view(B, L, C) for v in (x, z, dy)]
+    y, mean, rstd = m3.m3_group_norm_fwd(d[0], G, w.cuda(), b.cuda(), d[1], act=act, scope="sequence")
+    got = m3.m3_group_norm_bwd(d[0], G, mean, rstd, d[2], w.cuda(), b.cuda(), d[1], act=act, scope="sequence")
+    ok()
+    ref, tw, tb = parameter_bounds(x, z, dy, w, b, G, act, [(i * L, (i + 1) * L) for i in range(B)])
+    for name, tol, want in (("weight", tw, ref["w"]), ("bias", tb, ref["b"])):
+        assert tol.max() < 0.01 * np.sqrt((want ** 2).mean()), (name, tol.max())
+        assert (np.abs(f64(got[name]) - want) - tol).max() <= 0, name
