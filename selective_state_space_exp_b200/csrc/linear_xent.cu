@@ -598,12 +598,13 @@ xent_gemm_kernel(const GemmArgs g, const __grid_constant__ Maps maps) {
     }
   }
 
-  // every MMA issued has completed before TMEM is released (bounded)
+  // every MMA issued has completed before TMEM is released (bounded); of a pair each CTA
+  // waits on its own barrier, so that the other's arrival does not reach a CTA that is gone
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1 && rank == 0) {
-    if (elect_one()) commit<CG>(s_fin);
+  if (warp == 1) {
+    if (rank == 0 && elect_one()) commit<CG>(s_fin);
     __syncwarp();
     wait(s_fin, 0, g.status);
   }

@@ -148,3 +148,34 @@ def test_parameter_gradients_over_many_rows(B, L, G, cg, act, io):
     for name, tol, want in (("weight", tw, ref["w"]), ("bias", tb, ref["b"])):
         assert tol.max() < 0.01 * np.sqrt((want ** 2).mean()), (name, tol.max())
         assert (np.abs(f64(got[name]) - want) - tol).max() <= 0, name
+
+
+# ---- pairs of CTAs -----------------------------------------------------------------------
+
+def test_pairs_of_ctas_back_to_back():
+    """The loss in pairs of CTAs (at least 55 tiles of 256 x 256), again and again between
+    kernels that take the same SMs at once: the last arrivals of a pair reach it, not what
+    runs there next, and every repetition gives the same bits."""
+    g = gen(21)
+    h = torch.randn((600, 136), generator=g).bfloat16().cuda()
+    W = (torch.randn((9000, 136), generator=g) / 12).bfloat16().cuda()
+    t = torch.randint(0, 9000, (600,), generator=g).cuda()
+    dl = torch.rand(600, generator=g).cuda()
+    small = torch.randint(0, 1003, (77,), generator=g).cuda()
+    codes, scales, zeros = m3.m3_w4_quantize(W[:2048, :128].contiguous(), 64)
+
+    def step():
+        loss, lse = m3.m3_linear_xent_fwd(h, W, t)
+        out = m3.m3_linear_w4(h[:128, :128].contiguous(), codes, scales, zeros)
+        grads = m3.m3_linear_xent_bwd(h, W, t, lse, dl)
+        few = m3.m3_linear_xent_fwd(h[:77], W[:1003], small)
+        return (loss, lse, out, *grads, *few)
+
+    first = step()
+    ok()
+    ref = lm.xent(h, W, t)
+    assert np.abs(f64(first[1]) - ref["lse"]).max() < 1e-4
+    for _ in range(100):
+        again = step()
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+    ok()
