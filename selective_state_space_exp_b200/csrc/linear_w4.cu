@@ -570,7 +570,8 @@ cudaError_t launch_plan(const W4Args& a, const W4Plan& p, cudaStream_t s) {
   memset(&map, 0, sizeof(map));
   if (!encode_codes(&map, a, 16 * MT)) return cudaErrorInvalidValue;
   auto kern = w4_kernel<G, ZEROS, MT, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the same limit whatever the plan: another host thread may set it between this and the launch
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
   e = cudaGetDevice(&dev);

@@ -179,3 +179,37 @@ def test_pairs_of_ctas_back_to_back():
         again = step()
         assert all(torch.equal(a, b) for a, b in zip(first, again))
     ok()
+
+
+# ---- host threads --------------------------------------------------------------------------
+
+def test_w4_from_several_host_threads():
+    """Calls whose plans take different amounts of shared memory, from four threads at once
+    on streams of their own."""
+    import threading
+    g = gen(31)
+    cases = []
+    for K in (64, 512, 4096, 20480):
+        A = torch.randn((1, K), generator=g).bfloat16().cuda()
+        q = m3.m3_w4_quantize(torch.randn((48, K), generator=g).cuda(), 64)
+        cases.append((A, q, m3.m3_linear_w4(A, *q, out_dtype=torch.float32)))
+    ok()
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(len(cases))
+
+    def work(A, q, want, stream):
+        try:
+            start.wait(60)
+            outs = [m3.m3_linear_w4(A, *q, out_dtype=torch.float32, stream=stream) for _ in range(400)]
+            stream.synchronize()
+            assert all(torch.equal(o, want) for o in outs)
+        except Exception as e:  # noqa: BLE001  (reported by the test's own thread)
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(*c, torch.cuda.Stream())) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    ok()
+    assert not wrong, wrong
