@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) unit_fwd_kernel(const NormArgs a, co
 #pragma unroll
         for (int e = 0; e < P; ++e)
           y[e] = activate<ACT>(ffma2(ffma2(x[k][e], scale, shift), w[k][e], b[k][e]), z[e]);
-        if (M3_IN((py - static_cast<char*>(a.y)) + k * gap, a.batch * a.channels * X::ES, a.status))
+        if (M3_IN((py - static_cast<char*>(a.y)) + k * gap + V * X::ES - 1, a.batch * a.channels * X::ES, a.status))
           X::store(py + k * gap, 0, y);
       }
     }
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kThreads) unit_bwd_kernel(const NormArgs a, co
           c2 = ffma2(gw[k][e], xh[k][e], c2);
         }
         if (ACT == M3_ACT_GATE && dz &&
-            M3_IN(at + u * step + k * gap, a.batch * a.channels * X::ES, a.status))
+            M3_IN(at + u * step + k * gap + V * X::ES - 1, a.batch * a.channels * X::ES, a.status))
           X::store(dz + at + u * step + k * gap, 0, d);
       }
       const float2 c = unit_sum<LANES>(make_float2(c1.x + c1.y, c2.x + c2.y), L, s_red);
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreads) unit_bwd_kernel(const NormArgs a, co
           float2 d[P];
 #pragma unroll
           for (int e = 0; e < P; ++e) d[e] = ffma2(gw[k][e], s, ffma2(xh[k][e], k2, k1));
-          if (M3_IN(at + u * step + k * gap, a.batch * a.channels * X::ES, a.status))
+          if (M3_IN(at + u * step + k * gap + V * X::ES - 1, a.batch * a.channels * X::ES, a.status))
             X::store(dx + at + u * step + k * gap, 0, d);
         }
       }
@@ -452,8 +452,10 @@ __global__ void __launch_bounds__(kThreads) unit_bwd_kernel(const NormArgs a, co
       tw += s_sum[r * width + i];
       tb += s_sum[(p.ty + r) * width + i];
     }
-    if (a.part_w) a.part_w[(int64_t)blockIdx.y * a.channels + c] = tw;
-    if (a.part_b) a.part_b[(int64_t)blockIdx.y * a.channels + c] = tb;
+    const int64_t at = (int64_t)blockIdx.y * a.channels + c;
+    if (!M3_IN(at, (int64_t)p.yb * a.channels, a.status)) continue;
+    if (a.part_w) a.part_w[at] = tw;
+    if (a.part_b) a.part_b[at] = tb;
   }
 }
 
@@ -556,6 +558,11 @@ __device__ __forceinline__ Place place_of(const NormArgs& a, const SlicePlan& p)
 // Group `i` of the tile, among all (a.groups: none).
 __device__ __forceinline__ int64_t group_of(const NormArgs& a, const SlicePlan& p, const Place& o, int i) {
   return p.pieces > 1 ? o.tile / p.pieces : (int64_t)o.tile * p.gpt + i;
+}
+
+// Place of the block's partial sums of group g among all.
+__device__ __forceinline__ int64_t part_of(const NormArgs& a, const SlicePlan& p, const Place& o, int64_t g) {
+  return ((o.sample * a.groups + g) * p.splits + blockIdx.y) * p.pieces + o.piece;
 }
 
 // Rows of a thread.
@@ -716,6 +723,7 @@ __device__ __forceinline__ void stats_pass(const NormArgs& a, const SlicePlan& p
 // A slice's mean and 1 / deviation, also for the caller.
 __device__ __forceinline__ float2 finish_stats(const NormArgs& a, int64_t slice, const Moments& m) {
   const float rstd = m.n > 0.f ? rsqrtf(m.m2 / m.n + a.eps) : 0.f;
+  if (!M3_IN(slice, a.batch * a.groups, a.status)) return make_float2(0.f, 0.f);
   if (a.mean) a.mean[slice] = m.mean;
   if (a.rstd) a.rstd[slice] = rstd;
   return make_float2(m.mean, rstd);
@@ -728,7 +736,8 @@ __global__ void __launch_bounds__(kThreads, 4) slice_stats_kernel(const NormArgs
   const Place o = place_of(a, p);
   Moments* out = reinterpret_cast<Moments*>(a.ws);
   stats_pass<BF16, V, kRowsAhead>(a, p, o, [&](int, int64_t g, const Moments& m) {
-    out[((o.sample * a.groups + g) * p.splits + blockIdx.y) * p.pieces + o.piece] = m;
+    const int64_t at = part_of(a, p, o, g);
+    if (M3_IN(at, a.batch * a.groups * p.splits * p.pieces, a.status)) out[at] = m;
   });
 }
 
@@ -867,7 +876,8 @@ __device__ __forceinline__ void sums_pass(const NormArgs& a, const SlicePlan& p,
     if (!part || c0 + j >= end) continue;
     float v = 0.f;
     for (int r = 0; r < p.ty; ++r) v += s_col[(which * p.ty + r) * width + j];
-    part[prow * a.channels + c0 + j] = v;
+    if (M3_IN(prow * a.channels + c0 + j, a.batch * p.splits * a.channels, a.status))
+      part[prow * a.channels + c0 + j] = v;
   }
 }
 
@@ -878,7 +888,8 @@ slice_sums_kernel(const NormArgs a, const SlicePlan p, float2* csum) {
   wait_for_previous();
   const Place o = place_of(a, p);
   sums_pass<BF16, V, ACT, kBwdRowsAhead>(a, p, o, [&](int, int64_t g, float2 c) {
-    csum[((o.sample * a.groups + g) * p.splits + blockIdx.y) * p.pieces + o.piece] = c;
+    const int64_t at = part_of(a, p, o, g);
+    if (M3_IN(at, a.batch * a.groups * p.splits * p.pieces, a.status)) csum[at] = c;
   });
 }
 

@@ -326,7 +326,7 @@ __device__ __forceinline__ void store_outputs(const W4Args& a, int64_t m, int64_
       if (n + j < a.N) v[j] += __ldg(a.bias + n + j);
   }
   const int64_t at = m * a.N + n;
-  if (!M3_IN(at, a.M * a.N, a.status)) return;
+  if (!M3_IN(at + (a.N % 4 == 0 ? 3 : 0), a.M * a.N, a.status)) return;
   if (a.N % 4 == 0) {  // whole and aligned
     if (a.out_f32)
       *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
@@ -876,12 +876,12 @@ w4_tc_kernel(const W4Args a, const TcPlan p, const __grid_constant__ CUtensorMap
             float* o = static_cast<float*>(a.out) + at;
 #pragma unroll
             for (int i = 0; i < Cf::COLS; ++i, o += a.N)
-              if (i < left) *o = acc[i] + b;
+              if (i < left && M3_IN(at + i * a.N, a.M * a.N, a.status)) *o = acc[i] + b;
           } else {
             __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + at;
 #pragma unroll
             for (int i = 0; i < Cf::COLS; ++i, o += a.N)
-              if (i < left) *o = __float2bfloat16_rn(acc[i] + b);
+              if (i < left && M3_IN(at + i * a.N, a.M * a.N, a.status)) *o = __float2bfloat16_rn(acc[i] + b);
           }
         }
 #pragma unroll

@@ -310,7 +310,7 @@ __device__ __forceinline__ void copy_scored(const GemmArgs& g) {
 #pragma unroll 4
     for (int v = lane; v < nvec; v += 32) {
       const uint4 x = from[v];  // does not wait for the target
-      to[v] = live ? x : make_uint4(0u, 0u, 0u, 0u);
+      if (M3_IN(m * g.K + 8 * v + 7, g.M * g.K, g.status)) to[v] = live ? x : make_uint4(0u, 0u, 0u, 0u);
     }
   }
 }

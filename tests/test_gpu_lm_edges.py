@@ -213,3 +213,18 @@ def test_w4_from_several_host_threads():
         t.join()
     ok()
     assert not wrong, wrong
+
+
+# ---- the bounds-checked build ----------------------------------------------------------------
+
+def test_larger_forms_in_bounds():
+    """The forms that only larger calls take, through the bounds-checked build."""
+    import os
+    import subprocess
+    import sys
+    from selective_state_space_exp_b200 import _build
+    _build.build(debug=True)
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, os.path.join(here, "debug_bounds_lm_forms_child.py")],
+                       env=dict(os.environ, M3_LIBRARY="debug"), capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0 and "ALL OK" in r.stdout, r.stdout[-3000:] + r.stderr[-3000:]
