@@ -380,7 +380,8 @@ M3_API int m3_mimo_down_gate(const m3_shape* shape, const void* Y, const float* 
  *
  *   shape     batch >= 1 samples, seqlen >= 0 positions of each, channels,
  *             groups (channels % groups == 0), io_dtype, act, eps >= 0;
- *             batch * groups < 2^31.
+ *             batch * groups < 2^31, and as many blocks: a group wider than
+ *             256 vectors (of up to 16 bytes) counts once for each 256 begun.
  *   x, z, y   [batch][seqlen][channels] io dtype, 16-byte aligned; z with
  *             M3_ACT_GATE only (NULL otherwise).  y may be x or z itself;
  *             other overlaps are not allowed.

@@ -1196,12 +1196,16 @@ size_t group_norm_workspace(const NormArgs& a, bool backward) {
   return (p.whole ? 0 : slice_stat_bytes(a) + slice_csum_bytes(a, p)) + part_bytes(a, a.batch * p.splits);
 }
 
+bool group_norm_fits(const NormArgs& a) {
+  UnitPlan u;
+  return unit_plan(a, false, &u) || a.batch * slice_plan(a, false).tiles <= INT32_MAX;
+}
+
 cudaError_t group_norm_fwd_launch(const NormArgs& a0, cudaStream_t s) {
   NormArgs a = a0;
   UnitPlan u;
   if (unit_plan(a, false, &u)) return unit_launch(a, u, false, s);
   const SlicePlan p = slice_plan(a, false);
-  if (a.batch * p.tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)(a.batch * p.tiles), (unsigned)p.splits);
   if (p.whole)
     return with_shape(a, p.V, [&](auto bf16, auto v, auto act) {
@@ -1232,7 +1236,6 @@ cudaError_t group_norm_bwd_launch(const NormArgs& a0, cudaStream_t s) {
     return e != cudaSuccess ? e : param_reduce(a, u.yb, s);
   }
   const SlicePlan p = slice_plan(a, true);
-  if (a.batch * p.tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)(a.batch * p.tiles), (unsigned)p.splits);
   const int64_t slices = a.batch * a.groups;
   float2* means = reinterpret_cast<float2*>(a.ws);

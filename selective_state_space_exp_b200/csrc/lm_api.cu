@@ -123,6 +123,7 @@ int norm_call(const m3_norm_shape* s, const int32_t* cu, int64_t tokens, bool va
       if (zero[i] && cudaMemsetAsync(zero[i], 0, n[i], cs) != cudaSuccess) return M3_ERR_CUDA;
     return M3_OK;
   }
+  if (!group_norm_fits(a)) return M3_ERR_UNSUPPORTED;
   const size_t need = group_norm_workspace(a, backward);
   if (need > 0 && (!ws || ws_bytes < need || !is_aligned(ws, 256))) return M3_ERR_WORKSPACE;
   a.x = io.x; a.z = io.z; a.dy = io.dy; a.w = io.w; a.b = io.b;
@@ -215,6 +216,7 @@ M3_API int m3_group_norm_workspace_size(const m3_norm_shape* s, int backward, in
   NormArgs a = norm_args(s);
   const int32_t some = 0;  // which kernels a call takes depends on whether it is packed
   if (packed) a.cu_seqlens = &some;
+  if (s->seqlen > 0 && !group_norm_fits(a)) return M3_ERR_UNSUPPORTED;
   *bytes = s->seqlen == 0 ? 0 : group_norm_workspace(a, backward != 0);
   return M3_OK;
 }

@@ -90,6 +90,8 @@ struct NormArgs {
   int* status;
 };
 
+// Whether a grid holds the call's blocks (one or more a sample and tile of channels).
+bool group_norm_fits(const NormArgs& a);
 size_t group_norm_workspace(const NormArgs& a, bool backward);
 cudaError_t group_norm_fwd_launch(const NormArgs& a, cudaStream_t s);
 cudaError_t group_norm_bwd_launch(const NormArgs& a, cudaStream_t s);

@@ -226,3 +226,21 @@ def test_w4_without_inputs_is_refused():
     with pytest.raises(ValueError, match="0 inputs"):
         m3.m3_linear_w4(torch.zeros((1, 0), dtype=torch.bfloat16), torch.zeros((4, 0), dtype=torch.uint8),
                         torch.zeros((4, 1), dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("dt", [m3.M3_BF16, m3.M3_F32])
+def test_norm_of_more_blocks_than_a_grid_has(lib, dt):
+    """Groups so wide that a sample takes thousands of blocks: refused by the size query and by
+    the calls alike, not at the launch."""
+    n = ctypes.c_size_t()
+    for kw, packed in ((dict(batch=1 << 20, seqlen=2), False), (dict(batch=1 << 20, seqlen=1), False),
+                       (dict(batch=1 << 20, seqlen=2), True)):
+        s = norm_shape(channels=(1 << 24) + 8, groups=1, io_dtype=dt, **kw)  # 8193 blocks or more a sample
+        for back in (0, 1):
+            assert lib.m3_group_norm_workspace_size(ctypes.byref(s), back, int(packed), ctypes.byref(n)) == UNSUPPORTED
+        if packed:
+            continue
+        far = [(i + 1) << 50 for i in range(12)]
+        at = dict(x=far[0], w=far[1], b=far[2], mean=far[4], rstd=far[5], ws=far[6], dy=far[7], dw=far[9], db=far[10])
+        assert norm(lib, s, False, y=far[3], **at) == UNSUPPORTED
+        assert norm(lib, s, True, dx=far[8], **at) == UNSUPPORTED
