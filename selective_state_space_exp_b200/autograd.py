@@ -171,7 +171,9 @@ class M3GroupNorm(torch.autograd.Function):
     def backward(ctx, dy):
         cu, x, weight, bias, z, mean, rstd = ctx.saved_tensors
         dy = _aligned(dy.to(x.dtype))
-        kw = dict(weight=weight, bias=bias, z=z, act=ctx.act)
+        need = ctx.needs_input_grad[6:]
+        kw = dict(weight=weight, bias=bias, z=z, act=ctx.act, want_dx=need[0], want_dweight=need[1],
+                  want_dbias=need[2], want_dz=need[3])
         if cu is None:
             g = m3.m3_group_norm_bwd(x, ctx.groups, mean, rstd, dy, scope=ctx.scope, **kw)
         else:
@@ -179,12 +181,11 @@ class M3GroupNorm(torch.autograd.Function):
                                             max_seqlen=ctx.max_seqlen, **kw)
             # the gradients of rows outside every sequence: y there is x itself
             outside = _outside(cu, x.shape[0])
-            g["x"] = torch.where(outside, dy, g["x"])
-            if z is not None:
+            if need[0]:
+                g["x"] = torch.where(outside, dy, g["x"])
+            if need[3]:
                 g["z"] = torch.where(outside, torch.zeros_like(z), g["z"])
-        need = ctx.needs_input_grad[6:]
-        return (None,) * 6 + tuple(g.get(name) if want else None for name, want in
-                                   zip(("x", "weight", "bias", "z"), need))
+        return (None,) * 6 + tuple(g.get(name) for name in ("x", "weight", "bias", "z"))
 
 
 def _outside(cu_seqlens, total):

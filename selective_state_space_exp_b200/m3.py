@@ -667,7 +667,7 @@ def _norm_forward(fn, plan, pre, x, stat, weight, bias, z, act, y, workspace, st
     return y, mean, rstd
 
 
-def _norm_backward(fn, plan, pre, x, stat, mean, rstd, dy, weight, bias, z, act, workspace,
+def _norm_backward(fn, plan, pre, x, stat, mean, rstd, dy, weight, bias, z, act, want, workspace,
                    stream):
     shape, dt, dev, f32 = x.shape, x.dtype, _device_of(x), torch.float32
     if (z is not None) != (act == "gate"):
@@ -683,15 +683,14 @@ def _norm_backward(fn, plan, pre, x, stat, mean, rstd, dy, weight, bias, z, act,
     if ctx is not None:
         ctx.__enter__()
     try:
-        g = {"x": torch.empty_like(x), "weight": x.new_empty(shape[-1:], dtype=f32),
-             "bias": x.new_empty(shape[-1:], dtype=f32)}
-        pz = None
+        g = {"x": torch.empty_like(x) if want[0] else None,
+             "weight": x.new_empty(shape[-1:], dtype=f32) if want[1] else None,
+             "bias": x.new_empty(shape[-1:], dtype=f32) if want[2] else None}
         if z is not None:
-            g["z"] = torch.empty_like(x)
-            pz = g["z"].data_ptr()
+            g["z"] = torch.empty_like(x) if want[3] else None
         pws, nws, keep = _scratch(plan[1], workspace, dev)
-        status = getattr(load(), fn)(*args, g["x"].data_ptr() or None, g["weight"].data_ptr(),
-                                     g["bias"].data_ptr(), pz, pws, nws, st)
+        status = getattr(load(), fn)(*args, *(None if t is None else t.data_ptr() or None for t in (
+            g["x"], g["weight"], g["bias"], g.get("z"))), pws, nws, st)
     finally:
         if ctx is not None:
             ctx.__exit__(None, None, None)
@@ -716,14 +715,17 @@ def m3_group_norm_fwd(x, groups: int, weight=None, bias=None, z=None, *, act="no
 
 
 def m3_group_norm_bwd(x, groups: int, mean, rstd, dy, weight=None, bias=None, z=None, *,
-                      act="none", scope="token", workspace=None, stream=None):
+                      act="none", scope="token", want_dx=True, want_dweight=True, want_dbias=True,
+                      want_dz=True, workspace=None, stream=None):
     """Backward of m3_group_norm_fwd from its inputs and statistics: a dict of
-    x and (act "gate") z in the io dtype, weight and bias fp32 [C]."""
+    x and (act "gate") z in the io dtype, weight and bias fp32 [C] (None for one
+    that is not wanted)."""
     batch, seqlen = _norm_extent(x.shape, groups, scope)
     plan = _norm_plan(batch or 1, seqlen if batch else 0, x.shape[-1], groups, x.dtype, act, 0.0,
                       True, False)
     return _norm_backward("m3_group_norm_bwd", plan, (), x, (batch, groups), mean, rstd, dy,
-                          weight, bias, z, act, workspace, stream)
+                          weight, bias, z, act, (want_dx, want_dweight, want_dbias, want_dz),
+                          workspace, stream)
 
 
 def _norm_packed(cu_seqlens, x, groups, max_seqlen):
@@ -753,13 +755,16 @@ def m3_group_norm_fwd_varlen(cu_seqlens, x, groups: int, weight=None, bias=None,
 
 
 def m3_group_norm_bwd_varlen(cu_seqlens, x, groups: int, mean, rstd, dy, weight=None, bias=None,
-                             z=None, *, act="none", max_seqlen=None, workspace=None, stream=None):
+                             z=None, *, act="none", max_seqlen=None, want_dx=True,
+                             want_dweight=True, want_dbias=True, want_dz=True, workspace=None,
+                             stream=None):
     """Backward of m3_group_norm_fwd_varlen (the dict of m3_group_norm_bwd);
     rows of dx and dz outside every sequence are undefined."""
     S, L, pre = _norm_packed(cu_seqlens, x, groups, max_seqlen)
     plan = _norm_plan(S, L, x.shape[1], groups, x.dtype, act, 0.0, True, True)
     return _norm_backward("m3_group_norm_bwd_varlen", plan, pre, x, (S, groups), mean, rstd, dy,
-                          weight, bias, z, act, workspace, stream)
+                          weight, bias, z, act, (want_dx, want_dweight, want_dbias, want_dz),
+                          workspace, stream)
 
 
 # ---- the head's cross entropy ---------------------------------------------------

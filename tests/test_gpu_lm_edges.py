@@ -228,3 +228,38 @@ def test_larger_forms_in_bounds():
     r = subprocess.run([sys.executable, os.path.join(here, "debug_bounds_lm_forms_child.py")],
                        env=dict(os.environ, M3_LIBRARY="debug"), capture_output=True, text=True, timeout=900)
     assert r.returncode == 0 and "ALL OK" in r.stdout, r.stdout[-3000:] + r.stderr[-3000:]
+
+
+# ---- gradients that are not wanted, gradients that lie anywhere --------------------------------
+
+@pytest.mark.parametrize("L", [1, 30, 3000])
+def test_norm_gradients_that_are_not_wanted(L):
+    """Any set of the four gradients has the bits of the whole call (the forms of single
+    positions, of both passes in one block, of several splits)."""
+    g = gen(41 + L)
+    x, z, dy = (torch.randn((2, L, 48), generator=g).cuda() for _ in range(3))
+    w, b = torch.randn(48, generator=g).cuda(), torch.randn(48, generator=g).cuda()
+    kw = dict(act="gate", scope="sequence")
+    y, mean, rstd = m3.m3_group_norm_fwd(x, 2, w, b, z, **kw)
+    full = m3.m3_group_norm_bwd(x, 2, mean, rstd, dy, w, b, z, **kw)
+    names = ("x", "weight", "bias", "z")
+    for bits in range(16):
+        on = [bool(bits >> i & 1) for i in range(4)]
+        some = m3.m3_group_norm_bwd(x, 2, mean, rstd, dy, w, b, z, want_dx=on[0], want_dweight=on[1],
+                                    want_dbias=on[2], want_dz=on[3], **kw)
+        for name, want in zip(names, on):
+            assert torch.equal(some[name], full[name]) if want else some[name] is None, (bits, name)
+    ok()
+
+
+def test_norm_gradient_of_a_part_of_a_cat():
+    """torch.cat along the tokens hands the norm a gradient that starts off a 16-byte
+    boundary: 3 channels of 4 bytes."""
+    from selective_state_space_exp_b200 import autograd
+    x = torch.randn((5, 3), generator=gen(51)).cuda().requires_grad_()
+    w = torch.randn((6, 3), generator=gen(52)).cuda()
+    head = torch.zeros((1, 3), device="cuda")
+    (torch.cat([head, autograd.group_norm(x, 1)]) * w).sum().backward()
+    ok()
+    ref = lm.group_norm(x, 1, dy=w[1:])
+    assert np.abs(f64(x.grad) - ref["x"]).max() < 256 * U * ref["rstd"].max() * 8

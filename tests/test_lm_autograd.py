@@ -41,7 +41,8 @@ def calls(monkeypatch):
             leaves = [t.detach().clone().requires_grad_() for t in (x, weight, bias, z) if t is not None]
             at = dict(zip(names, leaves))
             y = _norm(at["x"], groups, at.get("weight"), at.get("bias"), at.get("z"), act)[0]
-            return dict(zip(names, torch.autograd.grad(y, leaves, dy)))
+            wants = dict(x="want_dx", weight="want_dweight", bias="want_dbias", z="want_dz")
+            return {n: t if kw[wants[n]] else None for n, t in zip(names, torch.autograd.grad(y, leaves, dy))}
 
     def loss_fwd(h, W, targets, **kw):
         logits = h.float() @ W.float().T
@@ -140,3 +141,17 @@ def test_gradients_off_a_16_byte_boundary_are_copied(calls, monkeypatch):
     torch.cat([torch.zeros((1, 2)), y, state]).square().sum().backward()
     for g in grads[0]:
         assert g.is_contiguous() and g.data_ptr() % 16 == 0
+
+
+@pytest.mark.parametrize("which", ["token", "packed"])
+def test_only_wanted_gradients_of_the_norm_are_asked_for(calls, which):
+    """A frozen norm, an input without a gradient: the backward leaves them out."""
+    f = norm_calls()[which]
+    names = ("want_dx", "want_dweight", "want_dbias", "want_dz")
+    for wanted in ((1, 0, 0, 0), (0, 1, 1, 0), (0, 0, 0, 1), (1, 1, 0, 1), (0, 0, 1, 0)):
+        args = [t.requires_grad_(bool(w)) for t, w in zip(
+            (randn(6, 8), randn(8), randn(8, seed=1), randn(6, 8, seed=2)), wanted)]
+        f(*args).square().sum().backward()
+        asked = calls.pop()
+        assert tuple(asked[n] for n in names) == tuple(map(bool, wanted))
+        assert all((t.grad is not None) == bool(w) for t, w in zip(args, wanted))
