@@ -4,6 +4,13 @@ Argument marshalling only: every step of the layer runs in the library's CUDA
 kernels.  torch supplies device memory and the current stream.  There is no
 fallback: if the library is missing or the tensors are not on a CUDA device,
 the calls raise.
+
+The norm, head-loss and 4-bit calls (m3_group_norm_*, m3_linear_xent_*,
+m3_linear_w4, m3_w4_quantize) take stream=: the call then runs on that stream,
+its outputs and workspace are made in that stream's memory pool (the calls of the
+layer make theirs in the current stream's), and every tensor of the call is
+recorded on both streams.  The caller orders the streams: the inputs' making
+before the call, and the call before its results are used.
 """
 from __future__ import annotations
 
@@ -551,6 +558,9 @@ def m3_mimo_down_gate(Y, w_down, z=None, *, out=None, stream=None):
 # Their calls can be as short as a few microseconds on the device, so the
 # marshalling below keeps to plain integers and looks shapes and workspace sizes
 # up once per set of extents.
+#
+# With stream=, tensors are recorded on that stream and on the current one, so each
+# may be let go as soon as its last use is launched.
 
 def _stream_on(stream, device):
     """Handle of `stream`, or of the current stream of `device`."""
@@ -570,6 +580,18 @@ def _elsewhere(stream, device):
     if device.index == torch.cuda.current_device():
         return None
     return torch.cuda.device(device)
+
+
+def _share(stream, device, *tensors):
+    """Of a call on an explicit stream: the memory of its tensors is not given
+    out again before what that stream, and the current one, do with them."""
+    here = torch.cuda.current_stream(device)
+    if here == stream:
+        return
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+            t.record_stream(here)
 
 
 def _device_of(t):
@@ -662,6 +684,8 @@ def _norm_forward(fn, plan, pre, x, stat, weight, bias, z, act, y, workspace, st
     finally:
         if ctx is not None:
             ctx.__exit__(None, None, None)
+    if stream is not None:
+        _share(stream, dev, x, weight, bias, z, y, mean, rstd, keep)
     if status:
         raise M3Error(fn, status)
     return y, mean, rstd
@@ -694,6 +718,8 @@ def _norm_backward(fn, plan, pre, x, stat, mean, rstd, dy, weight, bias, z, act,
     finally:
         if ctx is not None:
             ctx.__exit__(None, None, None)
+    if stream is not None:
+        _share(stream, dev, x, weight, bias, z, mean, rstd, dy, *g.values(), keep)
     if status:
         raise M3Error(fn, status)
     return g
@@ -749,6 +775,8 @@ def m3_group_norm_fwd_varlen(cu_seqlens, x, groups: int, weight=None, bias=None,
     cu_seqlens [S+1] int32 on the device; max_seqlen as m3_scan_fwd_varlen.
     Rows of y outside every sequence are left as they are."""
     S, L, pre = _norm_packed(cu_seqlens, x, groups, max_seqlen)
+    if stream is not None:
+        _share(stream, x.device, cu_seqlens)
     plan = _norm_plan(S, L, x.shape[1], groups, x.dtype, act, eps, False, True)
     return _norm_forward("m3_group_norm_fwd_varlen", plan, pre, x, (S, groups), weight, bias, z,
                          act, y, workspace, stream)
@@ -761,6 +789,8 @@ def m3_group_norm_bwd_varlen(cu_seqlens, x, groups: int, mean, rstd, dy, weight=
     """Backward of m3_group_norm_fwd_varlen (the dict of m3_group_norm_bwd);
     rows of dx and dz outside every sequence are undefined."""
     S, L, pre = _norm_packed(cu_seqlens, x, groups, max_seqlen)
+    if stream is not None:
+        _share(stream, x.device, cu_seqlens)
     plan = _norm_plan(S, L, x.shape[1], groups, x.dtype, act, 0.0, True, True)
     return _norm_backward("m3_group_norm_bwd_varlen", plan, pre, x, (S, groups), mean, rstd, dy,
                           weight, bias, z, act, (want_dx, want_dweight, want_dbias, want_dz),
@@ -811,6 +841,8 @@ def m3_linear_xent_fwd(h, W, targets, *, ignore_index: int = -100, workspace=Non
     finally:
         if ctx is not None:
             ctx.__exit__(None, None, None)
+    if stream is not None:
+        _share(stream, dev, h, W, targets, loss, lse, keep)
     if status:
         raise M3Error("m3_linear_xent_fwd", status)
     return loss, lse
@@ -839,6 +871,8 @@ def m3_linear_xent_bwd(h, W, targets, lse, dloss, *, ignore_index: int = -100, w
     finally:
         if ctx is not None:
             ctx.__exit__(None, None, None)
+    if stream is not None:
+        _share(stream, dev, h, W, targets, lse, dloss, dh, dW, keep)
     if status:
         raise M3Error("m3_linear_xent_bwd", status)
     return dh, dW
@@ -869,6 +903,8 @@ def m3_w4_quantize(W, group: int = 128, *, symmetric=False, stream=None):
     finally:
         if ctx is not None:
             ctx.__exit__(None, None, None)
+    if stream is not None:
+        _share(stream, dev, W, codes, scales, zeros)
     if status:
         raise M3Error("m3_w4_quantize", status)
     return codes, scales, zeros
@@ -915,6 +951,8 @@ def m3_linear_w4(A, codes, scales, zeros=None, bias=None, *, out=None, out_dtype
     finally:
         if ctx is not None:
             ctx.__exit__(None, None, None)
+    if stream is not None:
+        _share(stream, dev, A, codes, scales, zeros, bias, out)
     if status:
         raise M3Error("m3_linear_w4", status)
     return out

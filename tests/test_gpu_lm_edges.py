@@ -263,3 +263,74 @@ def test_norm_gradient_of_a_part_of_a_cat():
     ok()
     ref = lm.group_norm(x, 1, dy=w[1:])
     assert np.abs(f64(x.grad) - ref["x"]).max() < 256 * U * ref["rstd"].max() * 8
+
+
+# ---- explicit streams -----------------------------------------------------------------------------
+
+def stream_calls():
+    """Name: (inputs' maker, call of them on a stream)."""
+    g = gen(61)
+    x = torch.randn((900, 512), generator=g)
+    h = torch.randn((900, 512), generator=g).bfloat16()
+    W = (torch.randn((700, 512), generator=g) / 20).bfloat16()
+    t = torch.randint(0, 700, (900,), generator=g)
+    cu = torch.tensor([0, 400, 900], dtype=torch.int32)
+    codes = torch.randint(0, 256, (700, 256), generator=g, dtype=torch.uint8)
+    scales = (torch.rand((700, 8), generator=g) / 50).bfloat16()
+
+    def norm(x, stream):
+        y, m, r = m3.m3_group_norm_fwd(x, 4, stream=stream)
+        return (y, *m3.m3_group_norm_bwd(x, 4, m, r, x, stream=stream).values())
+
+    def packed(c, x, stream):
+        y, m, r = m3.m3_group_norm_fwd_varlen(c, x, 4, max_seqlen=500, stream=stream)
+        return (y, *m3.m3_group_norm_bwd_varlen(c, x, 4, m, r, x, max_seqlen=500, stream=stream).values())
+
+    def loss(h, W, t, stream):
+        out, lse = m3.m3_linear_xent_fwd(h, W, t, stream=stream)
+        return (out, *m3.m3_linear_xent_bwd(h, W, t, lse, torch.ones_like(out), stream=stream))
+
+    return {"norm": ((x,), norm), "packed": ((cu, x), packed), "loss": ((h, W, t), loss),
+            "w4": ((h, codes, scales), lambda *a, stream: (m3.m3_linear_w4(*a, stream=stream),)),
+            "quantize": ((W,), lambda W, stream: m3.m3_w4_quantize(W, 64, stream=stream))}
+
+
+@pytest.mark.parametrize("name", ["norm", "packed", "loss", "w4", "quantize"])
+def test_inputs_may_be_let_go_before_their_stream_has_run(name):
+    """The call waits on its stream behind other work; meanwhile its inputs are let go, and
+    what the current stream then makes does not land in their memory."""
+    host, call = stream_calls()[name]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    want = call(*[t.cuda() for t in host], stream=None)
+    inputs = [t.cuda() for t in host]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # a tenth of a second
+    got = call(*inputs, stream=side)
+    sizes = [(t.shape, t.dtype) for t in inputs]
+    del inputs
+    held = [torch.empty(s, dtype=d, device="cuda").view(torch.uint8).fill_(255) for s, d in sizes for _ in range(3)]
+    side.synchronize()
+    ok()
+    assert held and all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("name", ["norm", "packed", "loss", "w4", "quantize"])
+def test_outputs_may_be_let_go_before_the_current_stream_has_read_them(name):
+    host, call = stream_calls()[name]
+    side = torch.cuda.Stream()
+    inputs = [t.cuda() for t in host]
+    want = call(*inputs, stream=None)
+    torch.cuda.synchronize()
+    got = call(*inputs, stream=side)
+    side.synchronize()
+    torch.cuda._sleep(200_000_000)
+    copies = [t.clone() for t in got]          # behind the sleep
+    sizes = [(t.shape, t.dtype) for t in got]
+    del got
+    with torch.cuda.stream(side):
+        held = [torch.empty(s, dtype=d, device="cuda").view(torch.uint8).fill_(255) for s, d in sizes for _ in range(3)]
+    torch.cuda.synchronize()
+    ok()
+    assert held and all(torch.equal(a, b) for a, b in zip(want, copies))
