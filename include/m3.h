@@ -460,13 +460,17 @@ M3_API int m3_group_norm_bwd_varlen(const m3_norm_shape* shape, const int32_t* c
  *   dh [tokens][width], dW [vocab][width]  bf16, 16-byte aligned, rounded once
  *            from fp32 sums; either may be NULL.  The gradient of each logit is
  *            rounded to bf16 before the products that give dh and dW.
- *   workspace  as the size queries say, 256-byte aligned.
+ *   workspace  as the size queries say, 256-byte aligned: of the backward's two
+ *            the first is for both gradients, the second for those that are
+ *            wanted (the others' pointers being NULL in the call).
  * No output may overlap an input or another output.  The results of a call do
  * not depend on what else runs: every sum has a fixed order. */
 M3_API int m3_linear_xent_fwd_workspace_size(int64_t tokens, int64_t vocab, int64_t width,
                                              size_t* bytes);
 M3_API int m3_linear_xent_bwd_workspace_size(int64_t tokens, int64_t vocab, int64_t width,
                                              size_t* bytes);
+M3_API int m3_linear_xent_bwd_workspace_size_for(int64_t tokens, int64_t vocab, int64_t width,
+                                                 int want_dh, int want_dW, size_t* bytes);
 
 M3_API int m3_linear_xent_fwd(int64_t tokens, int64_t vocab, int64_t width, const void* h,
                               const void* W, const int64_t* targets, int64_t ignore_index,

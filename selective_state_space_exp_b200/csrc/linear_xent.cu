@@ -843,10 +843,11 @@ BwdPlan bwd_plan(const XentArgs& a) {
   p.dh = cut_of(a.M, a.K, p.piece, true);
   p.dw = cut_of(p.piece, a.K, a.M, true);
   p.d_bytes = align_up((size_t)a.M * p.ldd * 2, 256);
-  p.dh_bytes = p.pieces > 1 || p.dh.splits > 1
+  // sums of a gradient, and the copy of the hidden states for dW, only where it is wanted
+  p.dh_bytes = a.dh && (p.pieces > 1 || p.dh.splits > 1)
                    ? align_up((size_t)p.dh.splits * a.M * a.K * 4, 256) : 0;
-  p.dw_bytes = p.dw.splits > 1 ? align_up((size_t)p.dw.splits * p.piece * a.K * 4, 256) : 0;
-  p.h_bytes = align_up((size_t)a.M * a.K * 2, 256);
+  p.dw_bytes = a.dW && p.dw.splits > 1 ? align_up((size_t)p.dw.splits * p.piece * a.K * 4, 256) : 0;
+  p.h_bytes = a.dW ? align_up((size_t)a.M * a.K * 2, 256) : 0;
   return p;
 }
 
@@ -869,6 +870,7 @@ cudaError_t sum_splits(const float* part, int splits, int64_t n, const float* un
 size_t xent_workspace(const XentArgs& a, bool backward) {
   if (a.M == 0) return 0;
   if (!backward) return fwd_stat_bytes(a) + align_up((size_t)a.M * 4, 256);
+  if (!a.dh && !a.dW) return 0;
   const BwdPlan p = bwd_plan(a);
   return p.d_bytes + p.dh_bytes + p.dw_bytes + p.h_bytes + 256;
 }

@@ -143,13 +143,15 @@ int check_xent(int64_t M, int64_t V, int64_t K) {
   return M3_OK;
 }
 
-int xent_size(int64_t M, int64_t V, int64_t K, bool backward, size_t* bytes) {
+int xent_size(int64_t M, int64_t V, int64_t K, bool backward, bool dh, bool dW, size_t* bytes) {
   int st = check_xent(M, V, K);
   if (st != M3_OK) return st;
   if (!bytes) return M3_ERR_INVALID_ARGUMENT;
   XentArgs a;
   memset(&a, 0, sizeof(a));
   a.M = M; a.V = V; a.K = K;
+  a.dh = dh ? bytes : nullptr;  // whether they are set counts
+  a.dW = dW ? bytes : nullptr;
   *bytes = xent_workspace(a, backward);
   return M3_OK;
 }
@@ -266,12 +268,17 @@ M3_API int m3_group_norm_bwd_varlen(const m3_norm_shape* s, const int32_t* cu_se
 
 M3_API int m3_linear_xent_fwd_workspace_size(int64_t tokens, int64_t vocab, int64_t width,
                                              size_t* bytes) {
-  return xent_size(tokens, vocab, width, false, bytes);
+  return xent_size(tokens, vocab, width, false, false, false, bytes);
 }
 
 M3_API int m3_linear_xent_bwd_workspace_size(int64_t tokens, int64_t vocab, int64_t width,
                                              size_t* bytes) {
-  return xent_size(tokens, vocab, width, true, bytes);
+  return xent_size(tokens, vocab, width, true, true, true, bytes);
+}
+
+M3_API int m3_linear_xent_bwd_workspace_size_for(int64_t tokens, int64_t vocab, int64_t width,
+                                                 int want_dh, int want_dW, size_t* bytes) {
+  return xent_size(tokens, vocab, width, true, want_dh != 0, want_dW != 0, bytes);
 }
 
 M3_API int m3_linear_xent_fwd(int64_t tokens, int64_t vocab, int64_t width, const void* h,

@@ -112,6 +112,7 @@ struct XentArgs {
   char* ws;
   int* status;
 };
+// The backward's depends on which of dh and dW are set.
 size_t xent_workspace(const XentArgs& a, bool backward);
 cudaError_t xent_fwd_launch(const XentArgs& a, cudaStream_t s);
 cudaError_t xent_bwd_launch(const XentArgs& a, cudaStream_t s);

@@ -151,6 +151,8 @@ def load() -> ctypes.CDLL:
             i64 = ctypes.c_int64
             for name in ("m3_linear_xent_fwd_workspace_size", "m3_linear_xent_bwd_workspace_size"):
                 getattr(L, name).argtypes = [i64] * 3 + [ctypes.POINTER(ctypes.c_size_t)]
+            L.m3_linear_xent_bwd_workspace_size_for.argtypes = [i64] * 3 + [ctypes.c_int] * 2 + \
+                [ctypes.POINTER(ctypes.c_size_t)]
             L.m3_linear_xent_fwd.argtypes = [i64] * 3 + [vp] * 3 + [i64] + [vp] * 3 + \
                 [ctypes.c_size_t, vp]
             L.m3_linear_xent_bwd.argtypes = [i64] * 3 + [vp] * 3 + [i64] + [vp] * 5 + \
@@ -161,7 +163,8 @@ def load() -> ctypes.CDLL:
             for name in ("m3_group_norm_workspace_size", "m3_group_norm_fwd",
                          "m3_group_norm_fwd_varlen", "m3_group_norm_bwd",
                          "m3_group_norm_bwd_varlen", "m3_linear_xent_fwd_workspace_size",
-                         "m3_linear_xent_bwd_workspace_size", "m3_linear_xent_fwd",
+                         "m3_linear_xent_bwd_workspace_size",
+                         "m3_linear_xent_bwd_workspace_size_for", "m3_linear_xent_fwd",
                          "m3_linear_xent_bwd", "m3_linear_w4", "m3_w4_quantize"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
@@ -801,14 +804,21 @@ def m3_group_norm_bwd_varlen(cu_seqlens, x, groups: int, mean, rstd, dy, weight=
 
 @functools.lru_cache(maxsize=4096)
 def _xent_bytes(tokens, vocab, width):
-    """Workspace bytes of the forward and of the backward."""
-    n, m = ctypes.c_size_t(0), ctypes.c_size_t(0)
-    L = load()
+    """Workspace bytes of the forward."""
+    n = ctypes.c_size_t(0)
     _check("m3_linear_xent_fwd_workspace_size",
-           L.m3_linear_xent_fwd_workspace_size(tokens, vocab, width, ctypes.byref(n)))
-    _check("m3_linear_xent_bwd_workspace_size",
-           L.m3_linear_xent_bwd_workspace_size(tokens, vocab, width, ctypes.byref(m)))
-    return n.value, m.value
+           load().m3_linear_xent_fwd_workspace_size(tokens, vocab, width, ctypes.byref(n)))
+    return n.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _xent_bwd_bytes(tokens, vocab, width, want_dh, want_dW):
+    """Workspace bytes of the backward for the gradients that are wanted."""
+    n = ctypes.c_size_t(0)
+    _check("m3_linear_xent_bwd_workspace_size_for",
+           load().m3_linear_xent_bwd_workspace_size_for(tokens, vocab, width, int(want_dh),
+                                                        int(want_dW), ctypes.byref(n)))
+    return n.value
 
 
 def _xent_args(h, W, targets):
@@ -828,7 +838,7 @@ def m3_linear_xent_fwd(h, W, targets, *, ignore_index: int = -100, workspace=Non
     (loss, lse), fp32 and shaped like targets."""
     args = _xent_args(h, W, targets)
     dev = h.device
-    need = _xent_bytes(*args[:3])[0]
+    need = _xent_bytes(*args[:3])
     st, ctx = _stream_on(stream, dev), _elsewhere(stream, dev)
     if ctx is not None:
         ctx.__enter__()
@@ -857,7 +867,7 @@ def m3_linear_xent_bwd(h, W, targets, lse, dloss, *, ignore_index: int = -100, w
     dev = h.device
     plse = _addr("lse", lse, torch.float32, targets.shape, dev)
     pdl = _addr("dloss", dloss, torch.float32, targets.shape, dev)
-    need = _xent_bytes(*args[:3])[1]
+    need = _xent_bwd_bytes(*args[:3], bool(want_dh), bool(want_dW))
     st, ctx = _stream_on(stream, dev), _elsewhere(stream, dev)
     if ctx is not None:
         ctx.__enter__()

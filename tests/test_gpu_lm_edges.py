@@ -334,3 +334,28 @@ def test_outputs_may_be_let_go_before_the_current_stream_has_read_them(name):
     torch.cuda.synchronize()
     ok()
     assert held and all(torch.equal(a, b) for a, b in zip(want, copies))
+
+
+# ---- workspaces ---------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("M,V,K", [(300, 700, 64), (2000, 120, 1000), (20000, 15000, 16), (40, 9000, 1040)])
+def test_loss_workspace_of_the_wanted_gradients(M, V, K):
+    """dh or dW alone in a workspace of just its size, what lies behind it left as it was;
+    the bits are those of both at once (one piece, a split dW, three pieces, a split dh)."""
+    import ctypes
+    g = gen(71 + M)
+    h = torch.randn((M, K), generator=g).bfloat16().cuda()
+    W = (torch.randn((V, K), generator=g) / K ** 0.5).bfloat16().cuda()
+    t = torch.randint(0, V, (M,), generator=g).cuda()
+    t[::7] = -100
+    dl = torch.rand(M, generator=g).cuda()
+    loss, lse = m3.m3_linear_xent_fwd(h, W, t)
+    dh, dW = m3.m3_linear_xent_bwd(h, W, t, lse, dl)
+    n = ctypes.c_size_t()
+    for want in ((True, False), (False, True)):
+        assert m3.load().m3_linear_xent_bwd_workspace_size_for(M, V, K, *map(int, want), ctypes.byref(n)) == 0
+        whole = torch.full((n.value + 4096,), 0xAB, dtype=torch.uint8, device="cuda")
+        got = m3.m3_linear_xent_bwd(h, W, t, lse, dl, want_dh=want[0], want_dW=want[1], workspace=whole[:n.value])
+        ok()
+        assert (whole[n.value:] == 0xAB).all()
+        assert all(torch.equal(a, b) if w else a is None for a, b, w in zip(got, (dh, dW), want))

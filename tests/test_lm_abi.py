@@ -244,3 +244,34 @@ def test_norm_of_more_blocks_than_a_grid_has(lib, dt):
         at = dict(x=far[0], w=far[1], b=far[2], mean=far[4], rstd=far[5], ws=far[6], dy=far[7], dw=far[9], db=far[10])
         assert norm(lib, s, False, y=far[3], **at) == UNSUPPORTED
         assert norm(lib, s, True, dx=far[8], **at) == UNSUPPORTED
+
+
+def test_xent_workspace_is_for_the_wanted_gradients(lib):
+    """A frozen head's call holds no copy of the hidden states and no sums of dW."""
+    n = ctypes.c_size_t()
+
+    def size(M, V, K, dh, dW):
+        assert lib.m3_linear_xent_bwd_workspace_size_for(M, V, K, dh, dW, ctypes.byref(n)) == 0
+        return n.value
+
+    for M, V, K in ((10, 100, 64), (2000, 120, 1000), (16384, 50257, 2048), (40, 9000, 1040), (77, 1003, 256)):
+        assert lib.m3_linear_xent_bwd_workspace_size(M, V, K, ctypes.byref(n)) == 0
+        both = n.value
+        assert size(M, V, K, 1, 1) == both
+        assert both - size(M, V, K, 1, 0) >= M * K * 2
+        assert size(M, V, K, 1, 0) >= M * V * 2 or V > 8000     # d itself
+        assert M * K * 2 <= size(M, V, K, 0, 1) <= both
+        assert size(M, V, K, 0, 0) == 0
+        for want, out in (((1, 0), dict(dW=None)), ((0, 1), dict(dh=None))):
+            assert xent(lib, True, M=M, V=V, K=K, n=size(M, V, K, *want) - 1, **dict(far(), **out)) == WORKSPACE
+    assert size(0, 100, 64, 1, 1) == 0
+    # several pieces of the vocabulary: the running sum of dh is a part
+    assert size(16384, 50257, 2048, 1, 1) - size(16384, 50257, 2048, 0, 1) >= 16384 * 2048 * 4
+    assert lib.m3_linear_xent_bwd_workspace_size_for(10, 0, 64, 1, 1, ctypes.byref(n)) == INVALID
+    assert lib.m3_linear_xent_bwd_workspace_size_for(10, 100, 12, 1, 1, ctypes.byref(n)) == UNSUPPORTED
+    assert lib.m3_linear_xent_bwd_workspace_size_for(10, 100, 64, 1, 1, None) == INVALID
+
+
+def far():
+    """Addresses for xent() so far apart that the largest tensors do not overlap."""
+    return {k: (i + 1) << 40 for i, k in enumerate(("h", "W", "t", "lse", "ws", "dl", "dh", "dW"))} | {"loss": None}
