@@ -1127,12 +1127,9 @@ cudaError_t with_shape(const NormArgs& a, int V, F&& f) {
   }
 }
 
+// smem: of the backward's sums, 32 KB at most (two of every value that the block's threads hold).
 template <typename K, typename... Args>
 cudaError_t launch(K kernel, dim3 grid, size_t smem, cudaStream_t s, bool dependent, Args... args) {
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
   return launch_kernel(kernel, grid, kThreads, smem, s, dependent, 1, args...);
 }
 
