@@ -206,6 +206,8 @@ def group_norm_varlen(cu_seqlens, x, groups: int, weight=None, bias=None, z=None
                       eps: float = 1e-5, max_seqlen=None):
     """group_norm over the sequences of a packed batch (x [T][C]); rows outside
     every sequence pass through unchanged.  First derivatives only."""
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens holds no sequence")
     if max_seqlen is None:
         max_seqlen = int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item())
     return M3GroupNorm.apply(cu_seqlens, max_seqlen, groups, act, eps, "sequence", x, weight,

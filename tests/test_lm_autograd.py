@@ -155,3 +155,8 @@ def test_only_wanted_gradients_of_the_norm_are_asked_for(calls, which):
         asked = calls.pop()
         assert tuple(asked[n] for n in names) == tuple(map(bool, wanted))
         assert all((t.grad is not None) == bool(w) for t, w in zip(args, wanted))
+
+
+def test_packed_norm_without_sequences_is_refused(calls):
+    with pytest.raises(ValueError, match="no sequence"):
+        autograd.group_norm_varlen(torch.zeros(1, dtype=torch.int32), randn(3, 4), 2)
