@@ -474,7 +474,7 @@ struct Moments {
 };
 __device__ __forceinline__ Moments merge(const Moments& p, const Moments& q) {
   const float n = p.n + q.n;
-  if (n == 0.f) return Moments{0.f, 0.f, 0.f};
+  if (p.n == 0.f) return q;  // a quotient of equal counts need not come out as 1
   const float d = q.mean - p.mean, f = __fdividef(q.n, n);
   return Moments{n, fmaf(d, f, p.mean), p.m2 + q.m2 + d * d * p.n * f};
 }
@@ -681,8 +681,8 @@ __device__ __forceinline__ void stats_pass(const NormArgs& a, const SlicePlan& p
     float2 s1 = both(0.f), s2 = both(0.f), v[X::P];
     X::unpack(X::load(a.x, (o.base + o.r0 + o.ty) * a.channels + o.col), v);
 #pragma unroll
-    for (int e = 0; e < X::P; ++e) s1 = fadd2(s1, v[e]);
-    float ref = (s1.x + s1.y) * (1.f / V);
+    for (int e = 0; e < X::P; ++e) s1 = fadd2(s1, minus<V>(v[e], v[0].x));
+    float ref = fmaf(s1.x + s1.y, 1.f / V, v[0].x);  // of equal values the value itself
     s1 = both(0.f);
     float sq = 0.f;     // s2 of the rows before the last pause: short sums, then their sum
     int moved = AHEAD;  // rows at which the reference moves next

@@ -359,3 +359,34 @@ def test_loss_workspace_of_the_wanted_gradients(M, V, K):
         ok()
         assert (whole[n.value:] == 0xAB).all()
         assert all(torch.equal(a, b) if w else a is None for a, b, w in zip(got, (dh, dW), want))
+
+
+# ---- equal values, values that are not finite, over sequences ------------------------------------
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("B,L,G,cg", [(4, 128, 32, 64), (300, 40, 16, 64), (2, 3000, 2, 24), (3, 61, 1, 4100), (3, 1001, 6, 85)])
+def test_slices_of_equal_values(B, L, G, cg, io):
+    """A slice without spread, far from 0: the mean is its value exactly, and y the bias."""
+    v = (torch.randn((B, 1, G, 1), generator=gen(81)) * 3000).to(IO[io]).float()
+    x = v.expand(B, L, G, cg).reshape(B, L, G * cg).to(IO[io]).contiguous().cuda()
+    b = torch.randn(G * cg, generator=gen(82)).bfloat16().float()
+    y, mean, rstd = m3.m3_group_norm_fwd(x, G, bias=b.cuda(), scope="sequence")
+    ok()
+    assert torch.equal(mean.cpu(), v.view(B, G))
+    assert torch.equal(y.float().cpu(), b.expand(B, L, G * cg))
+
+
+@pytest.mark.parametrize("B,L,G,cg", [(4, 128, 32, 64), (300, 40, 16, 64), (2, 3000, 2, 24), (3, 1001, 6, 85)])
+def test_values_that_are_not_finite_stay_in_their_slice(B, L, G, cg):
+    x = torch.randn((B, L, G, cg), generator=gen(91))
+    x[0, 0, 0, 0], x[1, L - 1, G - 1, 3], x[-1, L // 2, 1, 1] = float("nan"), float("inf"), -float("inf")
+    clean = torch.randn((B, L, G, cg), generator=gen(91))
+    y, mean, rstd = m3.m3_group_norm_fwd(x.view(B, L, -1).cuda(), G, scope="sequence")
+    want = m3.m3_group_norm_fwd(clean.view(B, L, -1).cuda(), G, scope="sequence")
+    ok()
+    bad = ~torch.isfinite(x).all(3).all(1)                       # [B][G]
+    y, ref = y.view(B, L, G, cg).cpu(), want[0].view(B, L, G, cg).cpu()
+    for i, g in bad.nonzero().tolist():
+        assert not torch.isfinite(y[i, :, g]).any() and not torch.isfinite(rstd[i, g])
+    assert torch.equal(torch.where(bad[:, None, :, None], ref, y), ref)
+    assert torch.equal(torch.where(bad, want[2].cpu(), rstd.cpu()), want[2].cpu())
