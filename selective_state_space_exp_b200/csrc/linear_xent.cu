@@ -780,7 +780,9 @@ struct Cut {
 };
 
 // A product with M x N outputs, reduced over K in steps of 64.  Pairs of CTAs on
-// 256 x 256 tiles where these fill three quarters of the SMs or more; else single
+// 256 x 256 tiles where these fill three quarters of the SMs or more and have rows for
+// both CTAs (the loss forward of 64 tokens x 20000 classes x 256 16.3 us with pairs, 10.6
+// without; 128 x 32000 x 1024 22.1 and 15.7; 128 x 50257 x 2048 47.1 and 46.1); else single
 // ones, with the columns and the splits of the reduction for which the longest
 // CTA loads least (24, 32 or 48 KB a step; a step's time goes with that: 0.16 to
 // 0.42 us).  Splits are at least eight steps long, and the launch that adds them
@@ -789,7 +791,7 @@ struct Cut {
 // wide ones; logits of 28 x 10776 x 1744 15.4 us (middle) against 19.2 (wide); but
 // dh of 391 x 56104 x 3296 181 us (wide, two splits) against 280 (middle).
 Cut cut_of(int64_t M, int64_t N, int64_t K, bool split) {
-  if (ceil_div(M, 2 * kBM) * ceil_div(N, kWide) >= kPlanSms / 2 * 3 / 4) return Cut{2, kWide, 1};
+  if (M > kBM && ceil_div(M, 2 * kBM) * ceil_div(N, kWide) >= kPlanSms / 2 * 3 / 4) return Cut{2, kWide, 1};
   const int64_t mt = ceil_div(M, kBM), kb = ceil_div(K, kBK);
   Cut best{1, kWide, 1};
   int64_t least = INT64_MAX;
