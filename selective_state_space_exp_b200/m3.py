@@ -710,14 +710,18 @@ def _norm_backward(fn, plan, pre, x, stat, mean, rstd, dy, weight, bias, z, act,
     if ctx is not None:
         ctx.__enter__()
     try:
-        g = {"x": torch.empty_like(x) if want[0] else None,
-             "weight": x.new_empty(shape[-1:], dtype=f32) if want[1] else None,
-             "bias": x.new_empty(shape[-1:], dtype=f32) if want[2] else None}
+        dx = torch.empty_like(x) if want[0] else None
+        dw = x.new_empty(shape[-1:], dtype=f32) if want[1] else None
+        db = x.new_empty(shape[-1:], dtype=f32) if want[2] else None
+        dz = torch.empty_like(x) if z is not None and want[3] else None
+        g = {"x": dx, "weight": dw, "bias": db}
         if z is not None:
-            g["z"] = torch.empty_like(x) if want[3] else None
+            g["z"] = dz
         pws, nws, keep = _scratch(plan[1], workspace, dev)
-        status = getattr(load(), fn)(*args, *(None if t is None else t.data_ptr() or None for t in (
-            g["x"], g["weight"], g["bias"], g.get("z"))), pws, nws, st)
+        status = getattr(load(), fn)(*args, dx is not None and dx.data_ptr() or None,
+                                     dw is not None and dw.data_ptr() or None,
+                                     db is not None and db.data_ptr() or None,
+                                     dz is not None and dz.data_ptr() or None, pws, nws, st)
     finally:
         if ctx is not None:
             ctx.__exit__(None, None, None)
