@@ -20,16 +20,16 @@
 //                  w, b and the sums for dw, db stay in registers.
 //   slice kernels  everything else: partial sums over splits of a sample's
 //                  positions, joined by a small kernel, then a second pass that
-//                  applies them (its reads come from L2 where the tensors fit
-//                  there).  Blocks cover whole rows, so that what runs at one
-//                  time reads neighbouring memory.  (Slices held in the shared
-//                  memory of clusters, read once, measured slower: 56 against
-//                  54 us forward and 169 against 100 us backward at 8 x 2048 x
-//                  2048, for the clusters leave SMs idle between them.)  Short
-//                  samples: one block makes both passes.
+//                  applies them (from HBM again where the batch is larger than
+//                  L2: each pass goes over all of it).  Blocks cover whole rows,
+//                  so that what runs at one time reads neighbouring memory.
+//                  (Slices held in the shared memory of clusters, read once,
+//                  measured slower: 56 against 54 us forward and 169 against 100
+//                  us backward at 8 x 2048 x 2048, for the clusters leave SMs
+//                  idle between them.)  Short samples: one block makes both passes.
 // Measured in bf16: 16384 tokens x 4096 channels, 64 groups, with the gate 77 us
 // forward (5.2 TB/s) and 129 us backward (5.2 TB/s, 6 us of it the sums of dw and db);
-// 8 sequences x 2048 x 2048, 32 groups, SiLU 46 us forward and 86 us backward (each
+// 8 sequences x 2048 x 2048, 32 groups, SiLU 44 us forward and 83 us backward (each
 // of their four passes at 4.5 to 5 TB/s, two joining launches at about 5 us).
 // Statistics are fp32: in the unit kernels the mean first, then the deviations
 // from it (whose own mean corrects it) and their squares; in the others sums about a
@@ -512,10 +512,11 @@ constexpr int kRowsAhead = 4, kBwdRowsAhead = 2;
 // A block makes both passes over all rows of its sample where a thread has at most
 // this many: one launch and no partial sums, but fewer blocks.  Forward / backward
 // with SiLU, us, this form against splits: 4 x 128 x 2048 in bf16 (8 rows a thread)
-// 4.6 / 7.5 against 9.6 / 16.3; 16 x 256 x 2048 (32) 11.6 / 21.0 against 18.9 / 30.7;
-// 16 x 512 x 2048 (64) 19.7 / 45.9 against 25.0 / 50.6; 6 x 160 x 2400 (54) 8.4 / 19.5
-// against 11.2 / 17.9; 64 x 256 x 2048 (128) 51.8 / 110 against 47.7 / 89.6.  More rows
-// are in flight than above, for the blocks are few.
+// 4.6 / 7.7 against 9.6 / 16.3; 16 x 256 x 2048 (32) 11.8 / 20.8 against 18.9 / 30.7;
+// 64 x 256 x 2048 (128) 51.8 / 110 against 45.5 / 88.5.  Between them it depends on the
+// blocks: 16 x 512 x 2048 (64, 128 blocks) 20.1 / 45.9 against 23.8 / 47.4, 6 x 160 x 2400
+// (54, 48 blocks) 12.0 / 19.5 against 10.4 / 17.1; splits are taken there.  More rows are in
+// flight than above, for the blocks are few.
 constexpr int kWholeRows = 32;
 constexpr int kWholeAhead = 8, kWholeBwdAhead = 4;
 
@@ -671,7 +672,7 @@ __device__ __forceinline__ void tile_moments(const SlicePlan& p, const Moments& 
 // by 2 d, the squares hold at least 4 n d^2 and the move takes 2 n d^2 off.  Sums about the
 // group's first value (one pivot for the block) lost 1e-4 to 1e-3 of rstd where that value
 // was 300 deviations out, in an emulation of their order.  Forward in bf16 against them:
-// 8 x 2048 x 2048 44.3 us, as before; 16 x 256 x 2048 11.9 against 11.3.
+// 8 x 2048 x 2048 44.0 us, as before; 16 x 256 x 2048 11.8 against 11.3.
 template <bool BF16, int V, int AHEAD, typename F>
 __device__ __forceinline__ void stats_pass(const NormArgs& a, const SlicePlan& p, const Place& o, F&& f) {
   using X = Io<BF16, V>;
@@ -1194,6 +1195,7 @@ size_t group_norm_workspace(const NormArgs& a, bool backward) {
 }
 
 bool group_norm_fits(const NormArgs& a) {
+  if (a.cg <= kThreads) return true;  // no more tiles than groups
   UnitPlan u;
   return unit_plan(a, false, &u) || a.batch * slice_plan(a, false).tiles <= INT32_MAX;
 }

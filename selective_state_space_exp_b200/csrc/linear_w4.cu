@@ -27,11 +27,12 @@
 // Rounding: sums, scales' products and bias in fp32, out rounded once.
 //
 // Measured: one token, 50257 x 2048: 17.3 us (groups of 128), 20.4 us (of 32, zero
-// points): 3.0 TB/s of codes and scales.  What bounds it is taking the codes apart: a
-// word of eight takes three shifts, four masks and four subtractions, 230 instructions
-// in all for 16 x 128 codes, and issue slots are half used.  11 tokens 24.9 us, 32 tokens 25.7, 64 tokens 31.8, 128 tokens x 8192 x 4096 19.8 us: there the
-// decoding, the products and the sums of a step wait on one another.  One token, 4096 x
-// 2048: 5.5 us, most of it the start of a kernel and the way to memory and back.
+// points): 3.0 TB/s of codes and scales.  230 instructions for 16 x 128 codes, 88 of them
+// a word's shifts, masks and subtractions, the others loads, scales, zero points and
+// additions; issue slots are 53 % used, no unit is at its limit.  11 tokens 24.9 us, 32
+// tokens 25.7, 64 tokens 31.8, 128 tokens x 8192 x 4096 19.8 us: there the decoding, the
+// products and the sums of a step wait on one another.  One token, 4096 x 2048: 5.5 us,
+// most of it the start of a kernel and the way to memory and back.
 #include <cuda.h>  // CUtensorMap
 
 #include <cstring>

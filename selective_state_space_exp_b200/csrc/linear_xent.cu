@@ -26,10 +26,11 @@
 // reduction is split, the partial sums being added in a fixed order.
 //
 // Measured at 2048 tokens, 32000 classes, width 2048 (268 GFLOP a product), each alone:
-// stats 148 us, dlogits 171, dW 156, dh 157 (1.57 to 1.82 PFLOP/s, the tensor pipe 81 to
-// 95 % active); back to back the power limit makes it 843 us in all.  16384 tokens,
-// 50257 classes: 10.6 ms, 1.27 PFLOP/s.  4096 tokens, 32768 classes, width 1024, forward
-// alone: 215 us, where a tile's exponentials outlast half its products.
+// stats 167 us, dlogits 170, dW 174, dh 182 (1.47 to 1.61 PFLOP/s, the tensor pipe 92 to
+// 96 % active; a GPU at a higher clock took 148 for stats); back to back the power limit
+// makes it 845 us in all.  16384 tokens, 50257 classes: 10.6 to 10.9 ms, 1.24 to 1.27
+// PFLOP/s.  4096 tokens, 32768 classes, width 1024, forward alone: 214 to 219 us, where a
+// tile's exponentials outlast half its products.
 //
 // The tensor cores truncate addends as they align them to an fp32 accumulator: loss and
 // lse are good to about 2.5e-6 of their value at widths of 2700 and more.
