@@ -782,11 +782,12 @@ def m3_group_norm_fwd_varlen(cu_seqlens, x, groups: int, weight=None, bias=None,
     cu_seqlens [S+1] int32 on the device; max_seqlen as m3_scan_fwd_varlen.
     Rows of y outside every sequence are left as they are."""
     S, L, pre = _norm_packed(cu_seqlens, x, groups, max_seqlen)
+    plan = _norm_plan(S, L, x.shape[1], groups, x.dtype, act, eps, False, True)
+    out = _norm_forward("m3_group_norm_fwd_varlen", plan, pre, x, (S, groups), weight, bias, z,
+                        act, y, workspace, stream)
     if stream is not None:
         _share(stream, x.device, cu_seqlens)
-    plan = _norm_plan(S, L, x.shape[1], groups, x.dtype, act, eps, False, True)
-    return _norm_forward("m3_group_norm_fwd_varlen", plan, pre, x, (S, groups), weight, bias, z,
-                         act, y, workspace, stream)
+    return out
 
 
 def m3_group_norm_bwd_varlen(cu_seqlens, x, groups: int, mean, rstd, dy, weight=None, bias=None,
@@ -796,12 +797,13 @@ def m3_group_norm_bwd_varlen(cu_seqlens, x, groups: int, mean, rstd, dy, weight=
     """Backward of m3_group_norm_fwd_varlen (the dict of m3_group_norm_bwd);
     rows of dx and dz outside every sequence are undefined."""
     S, L, pre = _norm_packed(cu_seqlens, x, groups, max_seqlen)
+    plan = _norm_plan(S, L, x.shape[1], groups, x.dtype, act, 0.0, True, True)
+    out = _norm_backward("m3_group_norm_bwd_varlen", plan, pre, x, (S, groups), mean, rstd, dy,
+                         weight, bias, z, act, (want_dx, want_dweight, want_dbias, want_dz),
+                         workspace, stream)
     if stream is not None:
         _share(stream, x.device, cu_seqlens)
-    plan = _norm_plan(S, L, x.shape[1], groups, x.dtype, act, 0.0, True, True)
-    return _norm_backward("m3_group_norm_bwd_varlen", plan, pre, x, (S, groups), mean, rstd, dy,
-                          weight, bias, z, act, (want_dx, want_dweight, want_dbias, want_dz),
-                          workspace, stream)
+    return out
 
 
 # ---- the head's cross entropy ---------------------------------------------------
